@@ -304,6 +304,44 @@ poetx_status poetx_quantize_w0(const void* w, int64_t m, int64_t n, int32_t dtyp
 poetx_status poetx_dequantize_w0(const int8_t* wq, const float* scale, int64_t m, int64_t n,
                                  void* w_bf16, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * poetx_orthogonalize — an update orthogonalised by Newton-Schulz products (the step that the
+ *   Muon optimiser takes on a momentum matrix), for a stack of matrices:
+ *     X_0 = x / (|x|_F + eps);   X_{t+1} = a_t X_t + (b_t A + c_t A A) X_t,  A = X_t X_t^T;
+ *     out = scale * X_steps.
+ *   For x = U S V^T this is U p(S) V^T with p the composed odd quintics: with the coefficients
+ *   (3.4445, -4.7750, 2.0315) every singular value above ~1e-3 of the norm comes out near 1 in
+ *   five steps; (1.875, -1.25, 0.375) converges to 1 exactly, in more steps.
+ *   x [batch, m, n] (x_dtype, F32 or BF16), read only. out [batch, m, n] (out_dtype, F32 or
+ *   BF16); out may be x. m > n is worked on from the other side (same result).
+ *   coeffs: HOST array [steps][3] of (a_t, b_t, c_t), read before the call returns; steps in
+ *   1..POETX_ORTH_MAX_STEPS. eps >= 0: 0 / 0 for a matrix of zeros with eps = 0 gives NaN, as the
+ *   formula does; with eps > 0 zeros give zeros. The norm is summed in 64 bits. A matrix that
+ *   holds NaN or infinity gives NaN (in that matrix only).
+ *   Accuracy: F32 outputs to a few 2^-22 of the result's largest entry times the amplification
+ *   of the iteration; BF16 outputs to about one more bf16 rounding (operands are fp16 parts).
+ *   Deterministic: the same inputs give the same bits.
+ *   workspace >= poetx_orthogonalize_workspace_bytes(batch, m, n, steps) (0 for sizes that the call
+ *   refuses or that need no work).
+ *   Errors: INVALID_ARG (NULL, negative size, steps, eps, scale, coefficients that are not finite
+ *   or under which a singular value of [0, 1] passes 1e6), SHAPE (m or n > 65536, batch > 65535),
+ *   DTYPE, ALIGN, WORKSPACE, CUDA.
+ * poetx_orthogonalize_q — the same for an update of packed skew parameters: u and out
+ *   [nblocks, b(b-1)/2] fp32 (a dq of poetx_linear_bwd, or its momentum); every block is taken as
+ *   its skew b x b matrix (|X|_F^2 = 2 |u|^2), whose result is skew again. out may be u.
+ *   2 <= b <= 1024. Accuracy as for F32 outputs. Otherwise as poetx_orthogonalize.
+ * ------------------------------------------------------------------------------------------- */
+#define POETX_ORTH_MAX_STEPS 64
+size_t poetx_orthogonalize_workspace_bytes(int64_t batch, int64_t m, int64_t n, int32_t steps);
+poetx_status poetx_orthogonalize(const void* x, int32_t x_dtype, int64_t batch, int64_t m,
+                                 int64_t n, const float* coeffs, int32_t steps, float eps,
+                                 float scale, void* out, int32_t out_dtype, void* workspace,
+                                 size_t ws_bytes, void* stream);
+size_t poetx_orthogonalize_q_workspace_bytes(int64_t nblocks, int64_t b, int32_t steps);
+poetx_status poetx_orthogonalize_q(const float* u, int64_t nblocks, int64_t b, const float* coeffs,
+                                   int32_t steps, float eps, float scale, float* out,
+                                   void* workspace, size_t ws_bytes, void* stream);
+
 /* Draw the permutation that poetx_merge_reinit would use for (seed, lane) into perm [k]. */
 poetx_status poetx_resample_permutation(uint64_t seed, int32_t lane, int64_t k, int32_t* perm,
                                         void* stream);

@@ -7,7 +7,10 @@
 //   dA_j = dA'_j G_R^jT;  dG_R^j = A_j^T dA'_j;  dX[:, perm_r] = dA;  dq = CNP chain rule.
 #include "internal.h"
 #include "gemm.h"
+#include "orth.h"
 
+#include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdlib>
 #include <cstdio>
@@ -95,9 +98,18 @@ void set_pdl_attr(cudaLaunchAttribute& a) {
 // ------------------------------------------------------------------ device error word
 __device__ int g_device_error;
 
+// One word per device: a library call uses the word of the device that is current.
 int* device_error_word() {
-  static int* p = nullptr;
-  if (!p) cudaGetSymbolAddress(reinterpret_cast<void**>(&p), g_device_error);
+  constexpr int kDevices = 64;
+  static std::atomic<int*> words[kDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return nullptr;
+  int* p = words[dev].load(std::memory_order_acquire);
+  if (!p) {
+    if (cudaGetSymbolAddress(reinterpret_cast<void**>(&p), g_device_error) != cudaSuccess)
+      return nullptr;
+    words[dev].store(p, std::memory_order_release);
+  }
   return p;
 }
 
@@ -928,6 +940,102 @@ poetx_status poetx_merge_reinit(poetx_layer* L, uint64_t seed, void* workspace, 
   CHECK_CUDA(fill_zero_f32(L->q_r, m / b * (b * (b - 1) / 2), s), "zero q_r");
   CHECK_CUDA(fill_zero_f32(L->q_p, n / b * (b * (b - 1) / 2), s), "zero q_p");
   return POETX_OK;
+}
+
+// ------------------------------------------------------------------ Newton-Schulz
+namespace {
+
+// One Newton-Schulz problem and its argument checks, shared by the dense and the packed form.
+poetx_status check_orth(const char* what, orth::Problem* p, int64_t batch, int64_t m, int64_t n,
+                        const float* coeffs, int32_t steps, float eps, float scale,
+                        orth::Plan* plan) {
+  constexpr int64_t kMaxSide = 65536, kMaxBatch = 65535;
+  if (batch < 0 || m < 0 || n < 0)
+    return fail(POETX_ERR_INVALID_ARG, "%s: negative size", what);
+  if (batch > kMaxBatch || m > kMaxSide || n > kMaxSide ||
+      batch * ((m + 127) / 128) * ((n + 127) / 128) > (int64_t)INT32_MAX)
+    return fail(POETX_ERR_SHAPE, "%s: %lld matrices of %lld x %lld exceed the supported sizes", what,
+                (long long)batch, (long long)m, (long long)n);
+  if (!coeffs) return fail(POETX_ERR_INVALID_ARG, "%s: coeffs is NULL", what);
+  if (steps < 1 || steps > POETX_ORTH_MAX_STEPS)
+    return fail(POETX_ERR_INVALID_ARG, "%s: steps=%d is not in 1..%d", what, (int)steps,
+                POETX_ORTH_MAX_STEPS);
+  if (!(eps >= 0.f) || !std::isfinite(eps) || !std::isfinite(scale))
+    return fail(POETX_ERR_INVALID_ARG, "%s: eps must be finite and >= 0, scale finite", what);
+  if (!orth::make_plan(coeffs, steps, plan))
+    return fail(POETX_ERR_INVALID_ARG,
+                "%s: coefficients not finite, or the singular values pass 1e6 under them", what);
+  p->batch = batch; p->m = m; p->n = n;
+  p->steps = steps; p->coeffs = coeffs; p->eps = eps; p->scale = scale;
+  return POETX_OK;
+}
+
+poetx_status run_orth(const char* what, const orth::Problem& p, const orth::Plan& plan,
+                      const void* x, void* out, void* workspace, size_t ws_bytes, void* stream) {
+  if (!x || !out) return fail(POETX_ERR_INVALID_ARG, "%s: a pointer is NULL", what);
+  if (!aligned16(x) || !aligned16(out))
+    return fail(POETX_ERR_ALIGN, "%s: pointers must be 16-byte aligned", what);
+  poetx_status st = check_ws(workspace, ws_bytes, orth::workspace_bytes(p));
+  if (st != POETX_OK) return st;
+  if ((st = check_device()) != POETX_OK) return st;
+  CHECK_CUDA(orth::run(p, plan, x, out, workspace, as_stream(stream)), what);
+  return POETX_OK;
+}
+
+// The sizes of a workspace query; false where the call itself would refuse them.
+bool orth_sizes_ok(int64_t batch, int64_t m, int64_t n, int32_t steps) {
+  return batch > 0 && m > 0 && n > 0 && batch <= 65535 && m <= 65536 && n <= 65536 && steps >= 1 &&
+         steps <= POETX_ORTH_MAX_STEPS;
+}
+
+}  // namespace
+
+size_t poetx_orthogonalize_workspace_bytes(int64_t batch, int64_t m, int64_t n, int32_t steps) {
+  if (!orth_sizes_ok(batch, m, n, steps)) return 0;
+  orth::Problem p;
+  p.batch = batch; p.m = m; p.n = n; p.steps = steps;
+  return orth::workspace_bytes(p);
+}
+
+poetx_status poetx_orthogonalize(const void* x, int32_t x_dtype, int64_t batch, int64_t m,
+                                 int64_t n, const float* coeffs, int32_t steps, float eps,
+                                 float scale, void* out, int32_t out_dtype, void* workspace,
+                                 size_t ws_bytes, void* stream) {
+  if ((x_dtype != POETX_F32 && x_dtype != POETX_BF16) ||
+      (out_dtype != POETX_F32 && out_dtype != POETX_BF16))
+    return fail(POETX_ERR_DTYPE, "orthogonalize: unknown dtype");
+  orth::Problem p;
+  orth::Plan plan;
+  poetx_status st =
+      check_orth("orthogonalize", &p, batch, m, n, coeffs, steps, eps, scale, &plan);
+  if (st != POETX_OK) return st;
+  if (batch == 0 || m == 0 || n == 0) return POETX_OK;
+  p.in_t = dt_of(x_dtype);
+  p.out_t = dt_of(out_dtype);
+  return run_orth("orthogonalize", p, plan, x, out, workspace, ws_bytes, stream);
+}
+
+size_t poetx_orthogonalize_q_workspace_bytes(int64_t nblocks, int64_t b, int32_t steps) {
+  if (!orth_sizes_ok(nblocks, b, b, steps) || b < 2 || b > 1024) return 0;
+  orth::Problem p;
+  p.form = orth::Form::Skew;
+  p.batch = nblocks; p.m = p.n = b; p.steps = steps;
+  return orth::workspace_bytes(p);
+}
+
+poetx_status poetx_orthogonalize_q(const float* u, int64_t nblocks, int64_t b, const float* coeffs,
+                                   int32_t steps, float eps, float scale, float* out,
+                                   void* workspace, size_t ws_bytes, void* stream) {
+  if (b < 2) return fail(POETX_ERR_INVALID_ARG, "orthogonalize_q: b < 2");
+  if (b > 1024) return fail(POETX_ERR_SHAPE, "b=%lld exceeds 1024", (long long)b);
+  orth::Problem p;
+  orth::Plan plan;
+  poetx_status st =
+      check_orth("orthogonalize_q", &p, nblocks, b, b, coeffs, steps, eps, scale, &plan);
+  if (st != POETX_OK) return st;
+  if (nblocks == 0) return POETX_OK;
+  p.form = orth::Form::Skew;
+  return run_orth("orthogonalize_q", p, plan, u, out, workspace, ws_bytes, stream);
 }
 
 }  // extern "C"

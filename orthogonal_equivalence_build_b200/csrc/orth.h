@@ -1,0 +1,38 @@
+// Newton-Schulz orthogonalisation — interface of orth.cu.
+#pragma once
+#include "internal.h"
+
+namespace poetx {
+namespace orth {
+
+constexpr int kMaxSteps = 64;
+
+// Where the matrices come from and go to.
+enum class Form : int {
+  Dense = 0,   // batch x [m][n]
+  Skew = 1,    // batch x packed strict upper triangles of b x b skew matrices (m = n = b)
+};
+
+struct Problem {
+  Form form = Form::Dense;
+  int64_t batch = 0, m = 0, n = 0;
+  DT in_t = DT::F32, out_t = DT::F32;
+  int steps = 0;
+  const float* coeffs = nullptr;   // host, [steps][3]
+  float eps = 0.f, scale = 1.f;
+};
+
+// Powers of two that hold every operand of every step inside fp16 (see orth.cu).
+struct Plan {
+  float sx[kMaxSteps + 1];   // scale of X before step t
+  float sa[kMaxSteps], sh[kMaxSteps], sb[kMaxSteps];
+};
+// false: the coefficients are not finite or let the singular values grow past every bound
+bool make_plan(const float* coeffs, int steps, Plan* plan);
+
+size_t workspace_bytes(const Problem& p);
+cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, void* ws,
+                cudaStream_t s);
+
+}  // namespace orth
+}  // namespace poetx

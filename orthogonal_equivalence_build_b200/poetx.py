@@ -51,6 +51,7 @@ def _load() -> ctypes.CDLL:
     lib = ctypes.CDLL(LIB_PATH)
     V, I32, I64, U64, SZ = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64,
                             ctypes.c_size_t)
+    F = ctypes.c_float
     LP = ctypes.POINTER(Layer)
     sig = {
         "poetx_cnp_workspace_bytes": (SZ, [I64, I64]),
@@ -84,6 +85,10 @@ def _load() -> ctypes.CDLL:
         "poetx_status_string": (ctypes.c_char_p, [I32]),
         "poetx_last_error_message": (ctypes.c_char_p, []),
         "poetx_abi_version": (I32, []),
+        "poetx_orthogonalize_workspace_bytes": (SZ, [I64, I64, I64, I32]),
+        "poetx_orthogonalize": (I32, [V, I32, I64, I64, I64, V, I32, F, F, V, I32, V, SZ, V]),
+        "poetx_orthogonalize_q_workspace_bytes": (SZ, [I64, I64, I32]),
+        "poetx_orthogonalize_q": (I32, [V, I64, I64, V, I32, F, F, V, V, SZ, V]),
         "poetx_testing_gemm_bf16": (I32, [V, I64, I64, I32, V, I64, I64, I32, I64, I64, I64, V,
                                           I32, I64, I32, I32, U64, V]),
     }
@@ -106,7 +111,9 @@ EXPORTED = (
     "poetx_merge_permutations", "poetx_merge_reinit_workspace_bytes", "poetx_merge_reinit",
     "poetx_quantize_w0", "poetx_dequantize_w0", "poetx_resample_permutation", "poetx_validate_permutation", "poetx_device_status",
     "poetx_trace_enable", "poetx_trace_read", "poetx_trace_select", "poetx_status_string",
-    "poetx_last_error_message", "poetx_abi_version", "poetx_testing_gemm_bf16")
+    "poetx_last_error_message", "poetx_abi_version",
+    "poetx_orthogonalize_workspace_bytes", "poetx_orthogonalize",
+    "poetx_orthogonalize_q_workspace_bytes", "poetx_orthogonalize_q", "poetx_testing_gemm_bf16")
 
 
 def _check(status: int) -> None:
@@ -391,6 +398,112 @@ def trace_read(maxlen: int = 1 << 20):
         name, ms = line.rsplit(" ", 1)
         out.append((name, float(ms)))
     return out
+
+
+# ----------------------------------------------------------------------------- Newton-Schulz
+# The quintic (a, b, c) that the Muon optimiser uses, for every step.
+MUON_COEFFS = (3.4445, -4.7750, 2.0315)
+
+
+class _Call:
+    """The device and stream of one call, for tensors on any CUDA device: the tensors' own device
+    is made current, `stream` (default: that device's current stream) is the launch stream, and a
+    workspace allocated here belongs to that stream."""
+
+    def __init__(self, tensors, stream):
+        given = [t for t in tensors if t is not None]
+        self.device = given[0].device
+        if any(t.device != self.device for t in given):
+            raise ValueError("tensors of one call must be on one device")
+        if self.device.type != "cuda":
+            raise ValueError(f"tensors must be on a CUDA device, not {self.device}")
+        self._guard = torch.cuda.device(self.device)
+        self._stream = stream
+
+    def __enter__(self):
+        self._guard.__enter__()
+        s = self._stream
+        if s is None:
+            s = torch.cuda.current_stream(self.device)
+        elif not hasattr(s, "cuda_stream"):
+            s = torch.cuda.ExternalStream(int(s), device=self.device) if int(s) else \
+                torch.cuda.default_stream(self.device)
+        self._torch_stream = s
+        self.stream = s.cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        return self._guard.__exit__(*exc)
+
+    def workspace(self, nbytes: int, given: Optional[torch.Tensor]):
+        """(tensor, pointer, bytes); a given workspace is passed on as it is, for the library to
+        check."""
+        if given is not None:
+            return given, _ptr(given), given.numel() * given.element_size()
+        if nbytes == 0:
+            return None, None, 0
+        with torch.cuda.stream(self._torch_stream):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        return ws, ws.data_ptr(), nbytes
+
+
+def _coeff_array(coeffs, steps: int):
+    """[steps][3] floats from one (a, b, c) or from one per step."""
+    rows = [tuple(coeffs)] * steps if len(coeffs) == 3 and not hasattr(coeffs[0], "__len__") \
+        else [tuple(c) for c in coeffs]
+    if len(rows) != steps or any(len(r) != 3 for r in rows):
+        raise ValueError("coeffs must be one (a, b, c) or one per step")
+    flat = [float(v) for r in rows for v in r]
+    return (ctypes.c_float * len(flat))(*flat)
+
+
+def _matrices(x: torch.Tensor):
+    if x.dim() not in (2, 3):
+        raise ValueError("expected [m, n] or [batch, m, n]")
+    return (1, *x.shape) if x.dim() == 2 else tuple(x.shape)
+
+
+def orthogonalize_workspace_bytes(x: torch.Tensor, out: torch.Tensor, steps: int = 5) -> int:
+    batch, m, n = _matrices(x)
+    return int(lib.poetx_orthogonalize_workspace_bytes(batch, m, n, steps))
+
+
+def orthogonalize(x: torch.Tensor, out: torch.Tensor, steps: int = 5, coeffs=MUON_COEFFS,
+                  eps: float = 1e-7, scale: float = 1.0,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """out <- scale * NewtonSchulz(x) for x [m, n] or [batch, m, n], fp32 or bf16 each
+    (poetx_orthogonalize). coeffs: one (a, b, c) for every step, or one per step. out may be x."""
+    if out.shape != x.shape:
+        raise ValueError("out must have x's shape")
+    batch, m, n = _matrices(x)
+    c = _coeff_array(coeffs, steps)
+    with _Call((x, out, workspace), stream) as call:
+        ws, ptr, nbytes = call.workspace(
+            int(lib.poetx_orthogonalize_workspace_bytes(batch, m, n, steps)), workspace)
+        _check(lib.poetx_orthogonalize(_ptr(x), dtype_code(x.dtype), batch, m, n, c, steps, eps,
+                                       scale, _ptr(out), dtype_code(out.dtype), ptr, nbytes,
+                                       call.stream))
+
+
+def orthogonalize_q_workspace_bytes(nblocks: int, b: int, steps: int = 5) -> int:
+    return int(lib.poetx_orthogonalize_q_workspace_bytes(nblocks, b, steps))
+
+
+def orthogonalize_q(u: torch.Tensor, b: int, out: torch.Tensor, steps: int = 5,
+                    coeffs=MUON_COEFFS, eps: float = 1e-7, scale: float = 1.0,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """out <- scale * NewtonSchulz of every packed skew block of u [nblocks, b(b-1)/2] fp32
+    (poetx_orthogonalize_q). out may be u."""
+    if u.dtype != torch.float32 or out.dtype != torch.float32:
+        raise ValueError("packed skew parameters are fp32")
+    if u.dim() != 2 or u.shape[1] != b * (b - 1) // 2 or out.shape != u.shape:
+        raise ValueError("u and out must be [nblocks, b(b-1)/2]")
+    c = _coeff_array(coeffs, steps)
+    with _Call((u, out, workspace), stream) as call:
+        ws, ptr, nbytes = call.workspace(
+            int(lib.poetx_orthogonalize_q_workspace_bytes(u.shape[0], b, steps)), workspace)
+        _check(lib.poetx_orthogonalize_q(_ptr(u), u.shape[0], b, c, steps, eps, scale, _ptr(out),
+                                         ptr, nbytes, call.stream))
 
 
 def testing_gemm_bf16(a: torch.Tensor, a_mn: bool, b: torch.Tensor, b_mn: bool, M: int, N: int,
