@@ -342,6 +342,35 @@ poetx_status poetx_orthogonalize_q(const float* u, int64_t nblocks, int64_t b, c
                                    int32_t steps, float eps, float scale, float* out,
                                    void* workspace, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * poetx_layer_norm_fwd — layer norm of every row of x [T, m], as it stands in front of a linear:
+ *     mean = sum x / m;  rstd = 1 / sqrt(sum (x - mean)^2 / m + eps);
+ *     y = (x - mean) rstd gamma + beta.
+ *   x [T, m] and y [T, m] have `dtype`; y may be x. gamma, beta [m] have `w_dtype`; NULL stands
+ *   for ones and zeros. mean, rstd [T] fp32 outputs for the backward (either may be NULL).
+ *   Any T and m <= 2^20 (rows need not be a multiple of anything); sums are fp32, y is rounded
+ *   once. A row that holds NaN or infinity gives NaN in that row only; a constant row gives beta
+ *   up to rounding (with eps = 0 the formula is 0 / 0 there).
+ *   Errors: INVALID_ARG (NULL x or y, negative size, eps negative or not finite), SHAPE, DTYPE,
+ *   ALIGN, CUDA.
+ * poetx_layer_norm_bwd — its exact gradient for upstream dy [T, m], given the forward's x, mean
+ *   and rstd: with xh = (x - mean) rstd and g = dy gamma,
+ *     dx = rstd (g - sum g / m - xh sum(g xh) / m);  dgamma = sum_rows dy xh;  dbeta = sum_rows dy.
+ *   dx [T, m] (dtype; may be x or dy), dgamma, dbeta [m] fp32, each NULL to skip it. With
+ *   T = 0, dgamma and dbeta are zeros. The row sums are added in a fixed order: the same inputs
+ *   give the same bits.
+ *   workspace >= poetx_layer_norm_bwd_workspace_bytes(T, m); not used (may be NULL) when dgamma and
+ *   dbeta are both NULL. Errors: as the forward, plus WORKSPACE.
+ * ------------------------------------------------------------------------------------------- */
+poetx_status poetx_layer_norm_fwd(const void* x, int64_t T, int64_t m, int32_t dtype,
+                                  const void* gamma, const void* beta, int32_t w_dtype, float eps,
+                                  void* y, float* mean, float* rstd, void* stream);
+size_t poetx_layer_norm_bwd_workspace_bytes(int64_t T, int64_t m);
+poetx_status poetx_layer_norm_bwd(const void* x, const void* dy, int64_t T, int64_t m,
+                                  int32_t dtype, const void* gamma, int32_t w_dtype,
+                                  const float* mean, const float* rstd, void* dx, float* dgamma,
+                                  float* dbeta, void* workspace, size_t ws_bytes, void* stream);
+
 /* Draw the permutation that poetx_merge_reinit would use for (seed, lane) into perm [k]. */
 poetx_status poetx_resample_permutation(uint64_t seed, int32_t lane, int64_t k, int32_t* perm,
                                         void* stream);

@@ -7,6 +7,7 @@
 //   dA_j = dA'_j G_R^jT;  dG_R^j = A_j^T dA'_j;  dX[:, perm_r] = dA;  dq = CNP chain rule.
 #include "internal.h"
 #include "gemm.h"
+#include "norm.h"
 #include "orth.h"
 
 #include <atomic>
@@ -15,6 +16,7 @@
 #include <cstdlib>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -1036,6 +1038,79 @@ poetx_status poetx_orthogonalize_q(const float* u, int64_t nblocks, int64_t b, c
   if (nblocks == 0) return POETX_OK;
   p.form = orth::Form::Skew;
   return run_orth("orthogonalize_q", p, plan, u, out, workspace, ws_bytes, stream);
+}
+
+// ------------------------------------------------------------------ layer norm
+namespace {
+constexpr int64_t kMaxNormWidth = (int64_t)1 << 20;
+
+poetx_status check_norm(const char* what, int64_t T, int64_t m, int32_t dtype, int32_t w_dtype) {
+  if (T < 0 || m < 0) return fail(POETX_ERR_INVALID_ARG, "%s: negative size", what);
+  if (m > kMaxNormWidth)
+    return fail(POETX_ERR_SHAPE, "%s: m=%lld exceeds %lld", what, (long long)m,
+                (long long)kMaxNormWidth);
+  for (int32_t d : {dtype, w_dtype})
+    if (d != POETX_F32 && d != POETX_BF16)
+      return fail(POETX_ERR_DTYPE, "%s: unknown dtype %d", what, (int)d);
+  return POETX_OK;
+}
+
+poetx_status check_aligned(const char* what, std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return fail(POETX_ERR_ALIGN, "%s: pointer %p not 16-byte aligned", what, p);
+  return POETX_OK;
+}
+}  // namespace
+
+poetx_status poetx_layer_norm_fwd(const void* x, int64_t T, int64_t m, int32_t dtype,
+                                  const void* gamma, const void* beta, int32_t w_dtype, float eps,
+                                  void* y, float* mean, float* rstd, void* stream) {
+  poetx_status st = check_norm("layer_norm_fwd", T, m, dtype, w_dtype);
+  if (st != POETX_OK) return st;
+  if (!(eps >= 0.f) || !std::isfinite(eps))
+    return fail(POETX_ERR_INVALID_ARG, "layer_norm_fwd: eps must be finite and >= 0");
+  if (T == 0 || m == 0) return POETX_OK;
+  if (!x || !y) return fail(POETX_ERR_INVALID_ARG, "layer_norm_fwd: x or y is NULL");
+  if ((st = check_aligned("layer_norm_fwd", {x, gamma, beta, y, mean, rstd})) != POETX_OK) return st;
+  if ((st = check_device()) != POETX_OK) return st;
+  norm::Fwd a{x, T, m, gamma, beta, w_dtype == POETX_BF16, eps, y, mean, rstd};
+  CHECK_CUDA(norm::fwd(a, dt_of(dtype), as_stream(stream)), "layer_norm_fwd");
+  return POETX_OK;
+}
+
+size_t poetx_layer_norm_bwd_workspace_bytes(int64_t T, int64_t m) {
+  if (T <= 0 || m <= 0 || m > kMaxNormWidth) return 0;
+  return norm::bwd_ws_bytes(T, m);
+}
+
+poetx_status poetx_layer_norm_bwd(const void* x, const void* dy, int64_t T, int64_t m,
+                                  int32_t dtype, const void* gamma, int32_t w_dtype,
+                                  const float* mean, const float* rstd, void* dx, float* dgamma,
+                                  float* dbeta, void* workspace, size_t ws_bytes, void* stream) {
+  poetx_status st = check_norm("layer_norm_bwd", T, m, dtype, w_dtype);
+  if (st != POETX_OK) return st;
+  if (m == 0 || (!dx && !dgamma && !dbeta)) return POETX_OK;
+  if ((st = check_aligned("layer_norm_bwd", {x, dy, gamma, mean, rstd, dx, dgamma, dbeta})) !=
+      POETX_OK)
+    return st;
+  if (T == 0) {   // no rows: the sums over them are zero
+    if (!dgamma && !dbeta) return POETX_OK;
+    if ((st = check_device()) != POETX_OK) return st;
+    for (float* p : {dgamma, dbeta})
+      if (p) CHECK_CUDA(fill_zero_f32(p, m, as_stream(stream)), "layer_norm_bwd");
+    return POETX_OK;
+  }
+  if (!x || !dy || !mean || !rstd)
+    return fail(POETX_ERR_INVALID_ARG, "layer_norm_bwd: x, dy, mean or rstd is NULL");
+  // without column sums no scratch is used
+  const bool cols = dgamma || dbeta;
+  if (cols && (st = check_ws(workspace, ws_bytes, norm::bwd_ws_bytes(T, m))) != POETX_OK) return st;
+  if ((st = check_device()) != POETX_OK) return st;
+  norm::Bwd a{};
+  a.x = x; a.dy = dy; a.T = T; a.m = m; a.gamma = gamma; a.w_bf16 = w_dtype == POETX_BF16;
+  a.mean = mean; a.rstd = rstd; a.dx = dx; a.dgamma = dgamma; a.dbeta = dbeta;
+  CHECK_CUDA(norm::bwd(a, dt_of(dtype), workspace, as_stream(stream)), "layer_norm_bwd");
+  return POETX_OK;
 }
 
 }  // extern "C"

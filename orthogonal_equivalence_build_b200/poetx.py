@@ -85,6 +85,9 @@ def _load() -> ctypes.CDLL:
         "poetx_status_string": (ctypes.c_char_p, [I32]),
         "poetx_last_error_message": (ctypes.c_char_p, []),
         "poetx_abi_version": (I32, []),
+        "poetx_layer_norm_fwd": (I32, [V, I64, I64, I32, V, V, I32, F, V, V, V, V]),
+        "poetx_layer_norm_bwd_workspace_bytes": (SZ, [I64, I64]),
+        "poetx_layer_norm_bwd": (I32, [V, V, I64, I64, I32, V, I32, V, V, V, V, V, V, SZ, V]),
         "poetx_orthogonalize_workspace_bytes": (SZ, [I64, I64, I64, I32]),
         "poetx_orthogonalize": (I32, [V, I32, I64, I64, I64, V, I32, F, F, V, I32, V, SZ, V]),
         "poetx_orthogonalize_q_workspace_bytes": (SZ, [I64, I64, I32]),
@@ -112,6 +115,7 @@ EXPORTED = (
     "poetx_quantize_w0", "poetx_dequantize_w0", "poetx_resample_permutation", "poetx_validate_permutation", "poetx_device_status",
     "poetx_trace_enable", "poetx_trace_read", "poetx_trace_select", "poetx_status_string",
     "poetx_last_error_message", "poetx_abi_version",
+    "poetx_layer_norm_fwd", "poetx_layer_norm_bwd_workspace_bytes", "poetx_layer_norm_bwd",
     "poetx_orthogonalize_workspace_bytes", "poetx_orthogonalize",
     "poetx_orthogonalize_q_workspace_bytes", "poetx_orthogonalize_q", "poetx_testing_gemm_bf16")
 
@@ -400,11 +404,7 @@ def trace_read(maxlen: int = 1 << 20):
     return out
 
 
-# ----------------------------------------------------------------------------- Newton-Schulz
-# The quintic (a, b, c) that the Muon optimiser uses, for every step.
-MUON_COEFFS = (3.4445, -4.7750, 2.0315)
-
-
+# ----------------------------------------------------------------------------- layer norm
 class _Call:
     """The device and stream of one call, for tensors on any CUDA device: the tensors' own device
     is made current, `stream` (default: that device's current stream) is the launch stream, and a
@@ -445,6 +445,69 @@ class _Call:
         with torch.cuda.stream(self._torch_stream):
             ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         return ws, ws.data_ptr(), nbytes
+
+
+def _weights_code(weights, m: int) -> int:
+    """dtype code of the given norm weights (fp32 when there are none)."""
+    given = [w for w in weights if w is not None]
+    if any(tuple(w.shape) != (m,) for w in given):
+        raise ValueError("gamma and beta must be [m]")
+    if len({w.dtype for w in given}) > 1:
+        raise ValueError("gamma and beta must have one dtype")
+    return dtype_code(given[0].dtype) if given else F32
+
+
+def _check_outputs(shape, dtype, **outs) -> None:
+    for name, t in outs.items():
+        if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+            raise ValueError(f"{name} must be {list(shape)} {dtype}")
+
+
+def layer_norm_fwd(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor],
+                   y: torch.Tensor, mean: Optional[torch.Tensor] = None,
+                   rstd: Optional[torch.Tensor] = None, eps: float = 1e-5, stream=None) -> None:
+    """y [T, m] <- layer norm of x's rows; mean, rstd [T] fp32 for the backward
+    (poetx_layer_norm_fwd). y may be x."""
+    if x.dim() != 2:
+        raise ValueError("x must be [T, m]")
+    T, m = x.shape
+    _check_outputs(x.shape, x.dtype, y=y)
+    _check_outputs((T,), torch.float32, mean=mean, rstd=rstd)
+    wd = _weights_code((gamma, beta), m)
+    with _Call((x, gamma, beta, y, mean, rstd), stream) as call:
+        _check(lib.poetx_layer_norm_fwd(_ptr(x), T, m, dtype_code(x.dtype), _ptr(gamma),
+                                        _ptr(beta), wd, eps, _ptr(y), _ptr(mean), _ptr(rstd),
+                                        call.stream))
+
+
+def layer_norm_bwd_workspace_bytes(T: int, m: int) -> int:
+    return int(lib.poetx_layer_norm_bwd_workspace_bytes(T, m))
+
+
+def layer_norm_bwd(x: torch.Tensor, dy: torch.Tensor, gamma: Optional[torch.Tensor],
+                   mean: torch.Tensor, rstd: torch.Tensor, dx: Optional[torch.Tensor],
+                   dgamma: Optional[torch.Tensor] = None, dbeta: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """dx [T, m], dgamma, dbeta [m] fp32 (each None to skip it) for upstream dy and the forward's
+    x, mean and rstd (poetx_layer_norm_bwd). dx may be x or dy."""
+    if x.dim() != 2:
+        raise ValueError("x must be [T, m]")
+    T, m = x.shape
+    _check_outputs(x.shape, x.dtype, dy=dy, dx=dx)
+    _check_outputs((T,), torch.float32, mean=mean, rstd=rstd)
+    _check_outputs((m,), torch.float32, dgamma=dgamma, dbeta=dbeta)
+    wd = _weights_code((gamma,), m)
+    with _Call((x, dy, gamma, mean, rstd, dx, dgamma, dbeta, workspace), stream) as call:
+        need = 0 if dgamma is None and dbeta is None else layer_norm_bwd_workspace_bytes(T, m)
+        ws, ptr, nbytes = call.workspace(need, workspace)
+        _check(lib.poetx_layer_norm_bwd(_ptr(x), _ptr(dy), T, m, dtype_code(x.dtype),
+                                        _ptr(gamma), wd, _ptr(mean), _ptr(rstd), _ptr(dx),
+                                        _ptr(dgamma), _ptr(dbeta), ptr, nbytes, call.stream))
+
+
+# ----------------------------------------------------------------------------- Newton-Schulz
+# The quintic (a, b, c) that the Muon optimiser uses, for every step.
+MUON_COEFFS = (3.4445, -4.7750, 2.0315)
 
 
 def _coeff_array(coeffs, steps: int):
