@@ -42,11 +42,17 @@ namespace {
 using namespace umma;
 
 constexpr int BK = 64;
-constexpr int kStages = 6;
-constexpr int kThreads = 192;
+constexpr int kStages = 5;
+constexpr int kEpiWarps = 8;               // two per TMEM lane quarter, half of the columns each
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+// Registers per thread at launch, then of warps 0..3 (which only issue copies and MMAs) and of the
+// epilogue's: setmaxnreg moves them within what the block was launched with.
+constexpr int kRegsLaunch = 168, kRegsIssue = 56, kRegsEpi = 224;
+static_assert(128 * kRegsIssue + 32 * kEpiWarps * kRegsEpi <= kThreads * kRegsLaunch,
+              "the register split must fit the launch's registers");
 constexpr int kPartBytes = 128 * BK * 2;   // one operand of one CTA and stage: 128 rows x 64
 constexpr int kEpiStage = 8192;            // per epilogue warp
-constexpr size_t kSmem = (size_t)kStages * 2 * kPartBytes + 4 * kEpiStage + 1024 + 256;
+constexpr size_t kSmem = (size_t)kStages * 2 * kPartBytes + kEpiWarps * kEpiStage + 1024 + 256;
 
 // ------------------------------------------------------------------ products
 enum : int { kToMaps = 0, kRows = 1, kTransposed = 2, kPacked = 3 };
@@ -55,6 +61,7 @@ struct Prod {
   int tiles_m, tiles_n, per, total, sym, batch;
   int rows, cols;            // padded extents of the output (kToMaps)
   int nk, nseg;              // K blocks per segment; segment s multiplies parts pa[s], pb[s]
+  int chunk;                 // K blocks that one accumulator sums (see the kernel)
   int pa[3], pb[3];
   float f0, d0, f1, d1;      // output o: acc * f + (i == j) * d
   int has1, lo;              // a second output; both outputs in two parts
@@ -121,24 +128,46 @@ __device__ __forceinline__ constexpr uint32_t idesc() {
          ((uint32_t)(128 * CG >> 4) << 24);
 }
 
+// wait_bounded (umma_ptx.cuh) without the call: a call would put the accumulated registers on the
+// stack, and setmaxnreg allows none.
+__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, Ctl c, int code,
+                                            uint64_t limit_ns = kWaitLimitNs,
+                                            bool stop_on_abort = true) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 31) == 0) {
+      if (stop_on_abort && *c.abort) return false;
+      if (global_ns() - t0 > limit_ns) {
+        *c.abort = 1;
+        if (code) atomicCAS(c.err, 0, code);
+        return false;
+      }
+    }
+  }
+}
+
 // One 32-row x 64-column piece of a warp to the fp16 maps: both outputs, both parts, and the
 // mirrored piece of an off-diagonal tile. The warp's 8 KB stage is two halves that alternate, so
 // a piece is packed while the previous one's copy still reads its half.
-__device__ __forceinline__ void emit_maps(const Prod& p, const CUtensorMap* const (&maps)[2],
-                                          const CUtensorMap* const (&mmaps)[2],
-                                          const float (&v)[64], int g, int row0, int col0,
+__device__ __forceinline__ void emit_maps(const Prod& p, const CUtensorMap* out0,
+                                          const CUtensorMap* out1, const CUtensorMap* mir0,
+                                          const CUtensorMap* mir1,
+                                          const float* v, int g, int row0, int col0,
                                           bool mirror, uint8_t* stage, int lane, int& chunk) {
-  const int i = row0 + lane;
 #pragma unroll 1
   for (int o = 0; o <= p.has1; ++o) {
     const float f = o ? p.f1 : p.f0, d = o ? p.d1 : p.d0;
 #pragma unroll 1
     for (int part = 0; part <= p.lo; ++part) {
+      int dq = row0 + lane - col0;            // the diagonal's column of this row's 64
+      asm volatile("" : "+r"(dq));            // (not 64 comparisons kept over the loops)
       uint32_t h[32];
 #pragma unroll
       for (int q = 0; q < 32; ++q) {
-        float a = v[2 * q] * f + (i == col0 + 2 * q ? d : 0.f);
-        float b = v[2 * q + 1] * f + (i == col0 + 2 * q + 1 ? d : 0.f);
+        float a = v[2 * q] * f + (dq == 2 * q ? d : 0.f);
+        float b = v[2 * q + 1] * f + (dq == 2 * q + 1 ? d : 0.f);
         __half2 w = __floats2half2_rn(a, b);
         if (part) w = __floats2half2_rn(a - __low2float(w), b - __high2float(w));
         h[q] = *reinterpret_cast<uint32_t*>(&w);
@@ -154,7 +183,7 @@ __device__ __forceinline__ void emit_maps(const Prod& p, const CUtensorMap* cons
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
-        store_box(maps[o], smem_u32(half), col0, row0, z);
+        store_box(o ? out1 : out0, smem_u32(half), col0, row0, z);
         bulk_commit();
       }
       ++chunk;
@@ -173,7 +202,7 @@ __device__ __forceinline__ void emit_maps(const Prod& p, const CUtensorMap* cons
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          store_box(mmaps[o], smem_u32(half), row0, col0, z);
+          store_box(o ? mir1 : mir0, smem_u32(half), row0, col0, z);
           bulk_commit();
         }
         ++chunk;
@@ -188,16 +217,24 @@ __device__ __forceinline__ void put(void* out, long long at, float x, int f32) {
 }
 
 // The same piece to the caller's array.
-__device__ __forceinline__ void emit_user(const Prod& p, const float (&v)[64], int g, int row0,
+__device__ __forceinline__ void emit_user(const Prod& p, const float* v, int g, int row0,
                                           int col0, uint8_t* stage, int lane) {
   if (p.fmode == kTransposed) {
     // 32 rows of the piece are 32 neighbours of one output row
-    const int i = row0 + lane;
-    const long long base = ((long long)g * p.un + col0) * p.um + i;
+    const int i = row0 + lane, left = (int)min((long long)64, p.un - col0);
     if (i < p.um) {
+      const long long at = ((long long)g * p.un + col0) * p.um + i;
+      if (p.out_f32) {
+        float* o = static_cast<float*>(p.out) + at;
 #pragma unroll
-      for (int q = 0; q < 64; ++q)
-        if (col0 + q < p.un) put(p.out, base + (long long)q * p.um, v[q] * p.f0, p.out_f32);
+        for (int q = 0; q < 64; ++q, o += p.um)
+          if (q < left) *o = v[q] * p.f0;
+      } else {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
+#pragma unroll
+        for (int q = 0; q < 64; ++q, o += p.um)
+          if (q < left) *o = __float2bfloat16_rn(v[q] * p.f0);
+      }
     }
     return;
   }
@@ -257,7 +294,15 @@ __device__ __forceinline__ void emit_user(const Prod& p, const float (&v)[64], i
 // holds half of the tile's rows of A and half of its columns of B). A is K-major; B is K-major
 // (gram and square: B^T has A's layout) or N-major (update: B = X). Persistent and
 // warp-specialised: warp 0 streams operand tiles by TMA through a ring, one lane of warp 1
-// issues the MMAs into one of two accumulators, warps 2..5 store the other one.
+// issues the MMAs into one of two accumulators, warps 4..11 empty the other one (warps 2 and 3
+// complete the first register group).
+// The tensor core adds to its fp32 accumulator without rounding to nearest: every 16-deep step
+// loses up to a whole unit in the last place, always towards zero, and K = 2048 in three
+// passes came out 3.8e-5 off. So the parts' small products (hi lo, lo hi) come first, and for fp32
+// results an accumulator sums only p.chunk K blocks; the epilogue warps add the accumulators
+// in registers (round to nearest) while the next one fills: 128 x 256 sums of a CTA are 128
+// registers of eight warps, and emptying one takes a quarter of the time that 256 deep take to
+// compute.
 // Every wait is bounded; on expiry the device error word is set, the roles leave their loops,
 // copies and MMAs in flight are waited for (bounded) and TMEM is freed.
 template <int CG, bool B_MN>
@@ -274,7 +319,7 @@ ns_product_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_consta
   uint8_t* sa = smem;
   uint8_t* sb = smem + kStages * kPartBytes;
   uint8_t* sepi = sb + kStages * kPartBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sepi + 4 * kEpiStage);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sepi + kEpiWarps * kEpiStage);
   uint64_t* full = bars;              // leader only
   uint64_t* empty = bars + kStages;
   uint64_t* tfull = empty + kStages;  // [2]
@@ -297,7 +342,7 @@ ns_product_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_consta
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_u32(tfull + a), 1);
-      mbar_init(smem_u32(tempty + a), 4 * CG);
+      mbar_init(smem_u32(tempty + a), kEpiWarps * CG);
     }
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
@@ -327,134 +372,146 @@ ns_product_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_consta
   pdl_wait();      // the operands belong to the previous kernel of the stream
   pdl_trigger();
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      int it = 0;
-      bool ok = true;
-      for (int tile = first; ok && tile < p.total; tile += step) {
-        const Tile t = decode(p, tile);
-        const int am = t.mb * TILE + (int)rank * 128, bn = t.nb * TILE + (int)rank * 128;
-        for (int kb = 0; kb < nk; ++kb, ++it) {
-          const int s = it % kStages;
-          // stops only when the wait runs out: both CTAs of a pair are released by the same
-          // commits, so both have then issued the same loads
-          if (!wait_bounded(smem_u32(empty + s), ((uint32_t)(it / kStages) & 1u) ^ 1u, ctl,
-                            kErrProducer, kWaitLimitNs, /*stop_on_abort=*/false)) {
-            ok = false;
-            break;
-          }
-          const int seg = kb / p.nk, k = (kb - seg * p.nk) * BK;
-          const int za = p.pa[seg] * p.batch + t.g, zb = p.pb[seg] * p.batch + t.g;
-          uint32_t fb = smem_u32(full + s);
-          if (leader) mbar_expect_tx(fb, CG * 2 * kPartBytes);
-          if constexpr (CG == 2) fb = map_to_rank(fb, 0);
-          load_box<CG>(smem_u32(sa + s * kPartBytes), &tma_a, fb, k, am, za);
-          const uint32_t db = smem_u32(sb + s * kPartBytes);
-          if constexpr (B_MN) {
-            load_box<CG>(db, &tma_b, fb, bn, k, zb);
-            load_box<CG>(db + 64 * BK * 2, &tma_b, fb, bn + 64, k, zb);
-          } else {
-            load_box<CG>(db, &tma_b, fb, k, bn, zb);
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == 0) {
+      // ------------------------------------------------------------ TMA producer
+      if (lane == 0) {
+        int it = 0;
+        bool ok = true;
+        for (int tile = first; ok && tile < p.total; tile += step) {
+          const Tile t = decode(p, tile);
+          const int am = t.mb * TILE + (int)rank * 128, bn = t.nb * TILE + (int)rank * 128;
+          for (int kb = 0; kb < nk; ++kb, ++it) {
+            const int s = it % kStages;
+            // stops only when the wait runs out: both CTAs of a pair are released by the same
+            // commits, so both have then issued the same loads
+            if (!wait_inline(smem_u32(empty + s), ((uint32_t)(it / kStages) & 1u) ^ 1u, ctl,
+                             kErrProducer, kWaitLimitNs, /*stop_on_abort=*/false)) {
+              ok = false;
+              break;
+            }
+            const int seg = kb / p.nk, k = (kb - seg * p.nk) * BK;
+            const int za = p.pa[seg] * p.batch + t.g, zb = p.pb[seg] * p.batch + t.g;
+            uint32_t fb = smem_u32(full + s);
+            if (leader) mbar_expect_tx(fb, CG * 2 * kPartBytes);
+            if constexpr (CG == 2) fb = map_to_rank(fb, 0);
+            load_box<CG>(smem_u32(sa + s * kPartBytes), &tma_a, fb, k, am, za);
+            const uint32_t db = smem_u32(sb + s * kPartBytes);
+            if constexpr (B_MN) {
+              load_box<CG>(db, &tma_b, fb, bn, k, zb);
+              load_box<CG>(db + 64 * BK * 2, &tma_b, fb, bn + 64, k, zb);
+            } else {
+              load_box<CG>(db, &tma_b, fb, k, bn, zb);
+            }
           }
         }
+        if (!ok && leader)   // let the copies already issued land before the CTA leaves
+          for (int j = max(0, it - kStages); j < it; ++j)
+            wait_inline(smem_u32(full + j % kStages), (uint32_t)(j / kStages) & 1u, ctl, 0,
+                         kDrainLimitNs);
       }
-      if (!ok && leader)   // let the copies already issued land before the CTA leaves
-        for (int j = max(0, it - kStages); j < it; ++j)
-          wait_bounded(smem_u32(full + j % kStages), (uint32_t)(j / kStages) & 1u, ctl, 0,
-                       kDrainLimitNs);
+      __syncwarp();
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issuer
+      if (leader && lane == 0) {
+        constexpr uint32_t id = idesc<CG, B_MN>();
+        auto commit = [](uint32_t bar) {
+          if constexpr (CG == 2) umma_commit_pair_both(bar);
+          else umma_commit(bar);
+        };
+        int it = 0, count = 0;   // K blocks, accumulators
+        bool ok = true;
+        for (int tile = first; ok && tile < p.total; tile += step) {
+          for (int kb0 = 0; ok && kb0 < nk; kb0 += p.chunk, ++count) {
+            const int acc = count & 1, kb1 = min(nk, kb0 + p.chunk);
+            if (!wait_inline(smem_u32(tempty + acc), ((uint32_t)(count >> 1) & 1u) ^ 1u, ctl, kErrMma,
+                              kWaitLimitNs)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem_base + (uint32_t)(acc * TILE);
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+              const int s = it % kStages;
+              if (!wait_inline(smem_u32(full + s), (uint32_t)(it / kStages) & 1u, ctl, kErrMma,
+                                kWaitLimitNs)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t a0 = smem_u32(sa + s * kPartBytes), b0 = smem_u32(sb + s * kPartBytes);
+#pragma unroll
+              for (int kk = 0; kk < BK / 16; ++kk) {
+                const uint64_t ad = smem_desc(a0 + kk * 32, 16, 1024);
+                const uint64_t bd = B_MN ? smem_desc(b0 + kk * 2048, 64 * BK * 2, 1024)
+                                         : smem_desc(b0 + kk * 32, 16, 1024);
+                if constexpr (CG == 2) umma_bf16_pair(d, ad, bd, id, (kb > kb0 || kk > 0) ? 1u : 0u);
+                else umma_bf16(d, ad, bd, id, (kb > kb0 || kk > 0) ? 1u : 0u);
+              }
+              commit(smem_u32(empty + s));
+            }
+            if (ok) commit(smem_u32(tfull + acc));
+          }
+        }
+        commit(smem_u32(drain));   // every MMA of this thread has retired once this completes
+        wait_inline(smem_u32(drain), 0, ctl, ok ? kErrMma : 0, ok ? kWaitLimitNs : kDrainLimitNs);
+      }
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (leader && lane == 0) {
-      constexpr uint32_t id = idesc<CG, B_MN>();
-      auto commit = [](uint32_t bar) {
-        if constexpr (CG == 2) umma_commit_pair_both(bar);
-        else umma_commit(bar);
-      };
-      int it = 0, count = 0;
-      bool ok = true;
-      for (int tile = first; ok && tile < p.total; tile += step, ++count) {
+  } else {
+    // ------------------------------------------------------------ epilogue (warps 4..11)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+    constexpr int COLS = TILE / 2;        // this warp's columns of the tile
+    const int quarter = warp & 3;         // TMEM lanes 32 quarter .. + 31
+    const int cbase = ((warp - 4) >> 2) * COLS;
+    uint8_t* stage = sepi + (warp - 4) * kEpiStage;
+    uint32_t back = smem_u32(tempty);
+    if constexpr (CG == 2) back = map_to_rank(back, 0);
+    int count = 0, chunk = 0;
+    bool ok = true;
+    for (int tile = first; ok && tile < p.total; tile += step) {
+      const Tile t = decode(p, tile);
+      const int row0 = t.mb * TILE + (int)rank * 128 + quarter * 32;
+      const bool mirror = p.sym && t.mb != t.nb;
+      float v[COLS];
+#pragma unroll
+      for (int q = 0; q < COLS; ++q) v[q] = 0.f;
+      for (int kb0 = 0; kb0 < nk; kb0 += p.chunk, ++count) {
         const int acc = count & 1;
-        if (!wait_bounded(smem_u32(tempty + acc), ((uint32_t)(count >> 1) & 1u) ^ 1u, ctl, kErrMma,
-                          kWaitLimitNs)) {
+        if (!wait_inline(smem_u32(tfull + acc), (uint32_t)(count >> 1) & 1u, ctl, kErrEpilogue)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t d = tmem_base + (uint32_t)(acc * TILE);
-        for (int kb = 0; kb < nk; ++kb, ++it) {
-          const int s = it % kStages;
-          if (!wait_bounded(smem_u32(full + s), (uint32_t)(it / kStages) & 1u, ctl, kErrMma,
-                            kWaitLimitNs)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a0 = smem_u32(sa + s * kPartBytes), b0 = smem_u32(sb + s * kPartBytes);
+        const uint32_t trow = tmem_base + ((uint32_t)(quarter * 32) << 16) +
+                              (uint32_t)(acc * TILE + cbase);
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t ad = smem_desc(a0 + kk * 32, 16, 1024);
-            const uint64_t bd = B_MN ? smem_desc(b0 + kk * 2048, 64 * BK * 2, 1024)
-                                     : smem_desc(b0 + kk * 32, 16, 1024);
-            if constexpr (CG == 2) umma_bf16_pair(d, ad, bd, id, (kb > 0 || kk > 0) ? 1u : 0u);
-            else umma_bf16(d, ad, bd, id, (kb > 0 || kk > 0) ? 1u : 0u);
-          }
-          commit(smem_u32(empty + s));
+        for (int c = 0; c < COLS; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(trow + (uint32_t)c, r);
+#pragma unroll
+          for (int q = 0; q < 32; ++q) v[c + q] += __uint_as_float(r[q]);
         }
-        if (!ok) break;
-        commit(smem_u32(tfull + acc));
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 2) mbar_arrive_remote_relaxed(back + (uint32_t)(acc * 8));
+          else mbar_arrive(back + (uint32_t)(acc * 8));
+        }
       }
-      commit(smem_u32(drain));   // every MMA of this thread has retired once this completes
-      wait_bounded(smem_u32(drain), 0, ctl, ok ? kErrMma : 0, ok ? kWaitLimitNs : kDrainLimitNs);
-    }
-    __syncwarp();
-  } else {
-    // ------------------------------------------------------------ epilogue (warps 2..5)
-    const int quarter = warp & 3;   // TMEM lanes 32 quarter .. + 31
-    uint8_t* stage = sepi + (warp - 2) * kEpiStage;
-    const CUtensorMap* const maps[2] = {&out0, &out1};
-    const CUtensorMap* const mmaps[2] = {&mir0, &mir1};
-    uint32_t back = smem_u32(tempty);
-    if constexpr (CG == 2) back = map_to_rank(back, 0);
-    int count = 0, chunk = 0;
-    for (int tile = first; tile < p.total; tile += step, ++count) {
-      const Tile t = decode(p, tile);
-      const int acc = count & 1;
-      const int row0 = t.mb * TILE + (int)rank * 128 + quarter * 32;
-      const bool mirror = p.sym && t.mb != t.nb;
-      if (!wait_bounded(smem_u32(tfull + acc), (uint32_t)(count >> 1) & 1u, ctl, kErrEpilogue,
-                        kWaitLimitNs))
-        break;
-      tc_fence_after();
-      const uint32_t trow = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * TILE);
+      if (!ok) break;
       // pieces wholly in the padding (or below the diagonal of a packed result) are not stored
       const int rmax = p.fmode == kToMaps ? p.rows : (int)p.um;
       const int cmax = p.fmode == kToMaps ? p.cols : (int)p.un;
-#pragma unroll 1
-      for (int c = 0; c < TILE; c += 64) {
-        const int col0 = t.nb * TILE + c;
-        if (row0 >= rmax || col0 >= cmax || (p.fmode == kPacked && col0 + 63 <= row0)) continue;
-        uint32_t r0[32], r1[32];
-        tmem_ld32(trow + (uint32_t)c, r0);
-        tmem_ld32(trow + (uint32_t)(c + 32), r1);
-        float v[64];
 #pragma unroll
-        for (int q = 0; q < 32; ++q) {
-          v[q] = __uint_as_float(r0[q]);
-          v[32 + q] = __uint_as_float(r1[q]);
-        }
+      for (int c = 0; c < COLS; c += 64) {
+        const int col0 = t.nb * TILE + cbase + c;
+        if (row0 >= rmax || col0 >= cmax || (p.fmode == kPacked && col0 + 63 <= row0)) continue;
         if (p.fmode == kToMaps)
-          emit_maps(p, maps, mmaps, v, t.g, row0, col0, mirror, stage, lane, chunk);
+          emit_maps(p, &out0, &out1, &mir0, &mir1, v + c, t.g, row0, col0, mirror, stage, lane, chunk);
         else
-          emit_user(p, v, t.g, row0, col0, stage, lane);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (CG == 2) mbar_arrive_remote_relaxed(back + (uint32_t)(acc * 8));
-        else mbar_arrive(back + (uint32_t)(acc * 8));
+          emit_user(p, v + c, t.g, row0, col0, stage, lane);
       }
     }
     if (lane == 0) bulk_wait_all();   // every store written before the CTA leaves
@@ -680,6 +737,12 @@ cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const Stack* o0, 
   auto kern = ns_product_kernel<CG, B_MN>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
+  // setmaxnreg waits for registers that the block was not launched with: refuse such a build
+  static const int regs = [kern] {
+    cudaFuncAttributes a{};
+    return cudaFuncGetAttributes(&a, kern) == cudaSuccess ? a.numRegs : 0;
+  }();
+  if (regs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   set_pdl_attr(attr[0]);
@@ -794,6 +857,7 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
     q.total = (int)tiles(rows, cols, tile, sym);
     q.rows = (int)rows; q.cols = (int)cols;
     q.nk = (int)(K / BK);
+    q.chunk = exact ? 4 : q.nk * q.nseg;
     q.err = err;
     if (b_mn)
       return pair ? launch<2, true>(a, b, o0, o1, q, sms, name, s)
@@ -802,10 +866,10 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
                 : launch<1, false>(a, b, o0, o1, q, sms, name, s);
   };
   auto segments = [](Prod& q, int n) {
-    // hi hi; hi lo; lo hi
+    // hi hi | hi lo, hi hi | lo hi, hi lo, hi hi: small products first
     q.nseg = n;
-    const int pa[3] = {0, 0, 1}, pb[3] = {0, 1, 0};
-    for (int i = 0; i < 3; ++i) { q.pa[i] = pa[i]; q.pb[i] = pb[i]; }
+    const int pa[3] = {1, 0, 0}, pb[3] = {0, 1, 0};
+    for (int i = 0; i < n; ++i) { q.pa[i] = pa[3 - n + i]; q.pb[i] = pb[3 - n + i]; }
   };
 
   for (int t = 0; t < p.steps; ++t) {

@@ -405,62 +405,74 @@ def trace_read(maxlen: int = 1 << 20):
 
 
 # ----------------------------------------------------------------------------- layer norm
-class _Call:
-    """The device and stream of one call, for tensors on any CUDA device: the tensors' own device
-    is made current, `stream` (default: that device's current stream) is the launch stream, and a
-    workspace allocated here belongs to that stream."""
-
-    def __init__(self, tensors, stream):
-        given = [t for t in tensors if t is not None]
-        self.device = given[0].device
-        if any(t.device != self.device for t in given):
+def _device_of(*tensors) -> int:
+    """Index of the one CUDA device that the given tensors (None: skipped) live on."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != index:
             raise ValueError("tensors of one call must be on one device")
-        if self.device.type != "cuda":
-            raise ValueError(f"tensors must be on a CUDA device, not {self.device}")
-        self._guard = torch.cuda.device(self.device)
-        self._stream = stream
-
-    def __enter__(self):
-        self._guard.__enter__()
-        s = self._stream
-        if s is None:
-            s = torch.cuda.current_stream(self.device)
-        elif not hasattr(s, "cuda_stream"):
-            s = torch.cuda.ExternalStream(int(s), device=self.device) if int(s) else \
-                torch.cuda.default_stream(self.device)
-        self._torch_stream = s
-        self.stream = s.cuda_stream
-        return self
-
-    def __exit__(self, *exc):
-        return self._guard.__exit__(*exc)
-
-    def workspace(self, nbytes: int, given: Optional[torch.Tensor]):
-        """(tensor, pointer, bytes); a given workspace is passed on as it is, for the library to
-        check."""
-        if given is not None:
-            return given, _ptr(given), given.numel() * given.element_size()
-        if nbytes == 0:
-            return None, None, 0
-        with torch.cuda.stream(self._torch_stream):
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        return ws, ws.data_ptr(), nbytes
+    if index < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    return index
 
 
-def _weights_code(weights, m: int) -> int:
+def _raw_stream(stream, index: int) -> int:
+    """Launch stream of a call on device `index`: the given one or the device's current stream."""
+    if stream is None:
+        return torch.cuda.current_stream(index).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _scratch(nbytes: int, given: Optional[torch.Tensor], index: int, stream):
+    """(tensor, pointer, bytes) of a workspace. A given one is passed on as it is, for the library
+    to check; one allocated here belongs to the launch stream."""
+    if given is not None:
+        return given, _ptr(given), given.numel() * given.element_size()
+    if nbytes == 0:
+        return None, None, 0
+    if stream is None:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+    else:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=index) if int(stream) else \
+                torch.cuda.default_stream(index)
+        with torch.cuda.stream(stream):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+    return ws, ws.data_ptr(), nbytes
+
+
+def _run(index: int, fn, *args) -> None:
+    """Call the library with the tensors' device current."""
+    if torch.cuda.current_device() == index:
+        _check(fn(*args))
+    else:
+        with torch.cuda.device(index):
+            _check(fn(*args))
+
+
+def _weights_code(gamma, beta, m: int) -> int:
     """dtype code of the given norm weights (fp32 when there are none)."""
-    given = [w for w in weights if w is not None]
-    if any(tuple(w.shape) != (m,) for w in given):
-        raise ValueError("gamma and beta must be [m]")
-    if len({w.dtype for w in given}) > 1:
-        raise ValueError("gamma and beta must have one dtype")
-    return dtype_code(given[0].dtype) if given else F32
+    code = None
+    for w in (gamma, beta):
+        if w is None:
+            continue
+        if w.dim() != 1 or w.shape[0] != m:
+            raise ValueError("gamma and beta must be [m]")
+        c = dtype_code(w.dtype)
+        if code is not None and c != code:
+            raise ValueError("gamma and beta must have one dtype")
+        code = c
+    return F32 if code is None else code
 
 
-def _check_outputs(shape, dtype, **outs) -> None:
-    for name, t in outs.items():
-        if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
-            raise ValueError(f"{name} must be {list(shape)} {dtype}")
+def _check_like(name: str, t: Optional[torch.Tensor], x: torch.Tensor) -> None:
+    if t is not None and (t.shape != x.shape or t.dtype != x.dtype):
+        raise ValueError(f"{name} must be {list(x.shape)} {x.dtype}")
+
+
+def _check_vector(name: str, t: Optional[torch.Tensor], n: int) -> None:
+    if t is not None and (t.dim() != 1 or t.shape[0] != n or t.dtype != torch.float32):
+        raise ValueError(f"{name} must be [{n}] torch.float32")
 
 
 def layer_norm_fwd(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor],
@@ -471,13 +483,13 @@ def layer_norm_fwd(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optiona
     if x.dim() != 2:
         raise ValueError("x must be [T, m]")
     T, m = x.shape
-    _check_outputs(x.shape, x.dtype, y=y)
-    _check_outputs((T,), torch.float32, mean=mean, rstd=rstd)
-    wd = _weights_code((gamma, beta), m)
-    with _Call((x, gamma, beta, y, mean, rstd), stream) as call:
-        _check(lib.poetx_layer_norm_fwd(_ptr(x), T, m, dtype_code(x.dtype), _ptr(gamma),
-                                        _ptr(beta), wd, eps, _ptr(y), _ptr(mean), _ptr(rstd),
-                                        call.stream))
+    _check_like("y", y, x)
+    _check_vector("mean", mean, T)
+    _check_vector("rstd", rstd, T)
+    wd = _weights_code(gamma, beta, m)
+    dev = _device_of(x, gamma, beta, y, mean, rstd)
+    _run(dev, lib.poetx_layer_norm_fwd, _ptr(x), T, m, dtype_code(x.dtype), _ptr(gamma), _ptr(beta),
+         wd, eps, _ptr(y), _ptr(mean), _ptr(rstd), _raw_stream(stream, dev))
 
 
 def layer_norm_bwd_workspace_bytes(T: int, m: int) -> int:
@@ -493,16 +505,20 @@ def layer_norm_bwd(x: torch.Tensor, dy: torch.Tensor, gamma: Optional[torch.Tens
     if x.dim() != 2:
         raise ValueError("x must be [T, m]")
     T, m = x.shape
-    _check_outputs(x.shape, x.dtype, dy=dy, dx=dx)
-    _check_outputs((T,), torch.float32, mean=mean, rstd=rstd)
-    _check_outputs((m,), torch.float32, dgamma=dgamma, dbeta=dbeta)
-    wd = _weights_code((gamma,), m)
-    with _Call((x, dy, gamma, mean, rstd, dx, dgamma, dbeta, workspace), stream) as call:
-        need = 0 if dgamma is None and dbeta is None else layer_norm_bwd_workspace_bytes(T, m)
-        ws, ptr, nbytes = call.workspace(need, workspace)
-        _check(lib.poetx_layer_norm_bwd(_ptr(x), _ptr(dy), T, m, dtype_code(x.dtype),
-                                        _ptr(gamma), wd, _ptr(mean), _ptr(rstd), _ptr(dx),
-                                        _ptr(dgamma), _ptr(dbeta), ptr, nbytes, call.stream))
+    _check_like("dy", dy, x)
+    _check_like("dx", dx, x)
+    for name, t, n in (("mean", mean, T), ("rstd", rstd, T), ("dgamma", dgamma, m),
+                       ("dbeta", dbeta, m)):
+        _check_vector(name, t, n)
+    wd = _weights_code(gamma, None, m)
+    dev = _device_of(x, dy, gamma, mean, rstd, dx, dgamma, dbeta, workspace)
+    need = 0
+    if workspace is None and (dgamma is not None or dbeta is not None):
+        need = layer_norm_bwd_workspace_bytes(T, m)
+    ws, ptr, nbytes = _scratch(need, workspace, dev, stream)
+    _run(dev, lib.poetx_layer_norm_bwd, _ptr(x), _ptr(dy), T, m, dtype_code(x.dtype), _ptr(gamma),
+         wd, _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dgamma), _ptr(dbeta), ptr, nbytes,
+         _raw_stream(stream, dev))
 
 
 # ----------------------------------------------------------------------------- Newton-Schulz
@@ -540,12 +556,11 @@ def orthogonalize(x: torch.Tensor, out: torch.Tensor, steps: int = 5, coeffs=MUO
         raise ValueError("out must have x's shape")
     batch, m, n = _matrices(x)
     c = _coeff_array(coeffs, steps)
-    with _Call((x, out, workspace), stream) as call:
-        ws, ptr, nbytes = call.workspace(
-            int(lib.poetx_orthogonalize_workspace_bytes(batch, m, n, steps)), workspace)
-        _check(lib.poetx_orthogonalize(_ptr(x), dtype_code(x.dtype), batch, m, n, c, steps, eps,
-                                       scale, _ptr(out), dtype_code(out.dtype), ptr, nbytes,
-                                       call.stream))
+    dev = _device_of(x, out, workspace)
+    need = 0 if workspace is not None else orthogonalize_workspace_bytes(x, out, steps)
+    ws, ptr, nbytes = _scratch(need, workspace, dev, stream)
+    _run(dev, lib.poetx_orthogonalize, _ptr(x), dtype_code(x.dtype), batch, m, n, c, steps, eps,
+         scale, _ptr(out), dtype_code(out.dtype), ptr, nbytes, _raw_stream(stream, dev))
 
 
 def orthogonalize_q_workspace_bytes(nblocks: int, b: int, steps: int = 5) -> int:
@@ -562,11 +577,11 @@ def orthogonalize_q(u: torch.Tensor, b: int, out: torch.Tensor, steps: int = 5,
     if u.dim() != 2 or u.shape[1] != b * (b - 1) // 2 or out.shape != u.shape:
         raise ValueError("u and out must be [nblocks, b(b-1)/2]")
     c = _coeff_array(coeffs, steps)
-    with _Call((u, out, workspace), stream) as call:
-        ws, ptr, nbytes = call.workspace(
-            int(lib.poetx_orthogonalize_q_workspace_bytes(u.shape[0], b, steps)), workspace)
-        _check(lib.poetx_orthogonalize_q(_ptr(u), u.shape[0], b, c, steps, eps, scale, _ptr(out),
-                                         ptr, nbytes, call.stream))
+    dev = _device_of(u, out, workspace)
+    need = 0 if workspace is not None else orthogonalize_q_workspace_bytes(u.shape[0], b, steps)
+    ws, ptr, nbytes = _scratch(need, workspace, dev, stream)
+    _run(dev, lib.poetx_orthogonalize_q, _ptr(u), u.shape[0], b, c, steps, eps, scale, _ptr(out),
+         ptr, nbytes, _raw_stream(stream, dev))
 
 
 def testing_gemm_bf16(a: torch.Tensor, a_mn: bool, b: torch.Tensor, b_mn: bool, M: int, N: int,
