@@ -50,6 +50,7 @@ constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kRegsLaunch = 168, kRegsIssue = 56, kRegsEpi = 224;
 static_assert(128 * kRegsIssue + 32 * kEpiWarps * kRegsEpi <= kThreads * kRegsLaunch,
               "the register split must fit the launch's registers");
+constexpr int kChunk = 2;                  // K blocks per accumulator of an fp32 result
 constexpr int kPartBytes = 128 * BK * 2;   // one operand of one CTA and stage: 128 rows x 64
 constexpr int kEpiStage = 8192;            // per epilogue warp
 constexpr size_t kSmem = (size_t)kStages * 2 * kPartBytes + kEpiWarps * kEpiStage + 1024 + 256;
@@ -61,7 +62,7 @@ struct Prod {
   int tiles_m, tiles_n, per, total, sym, batch;
   int rows, cols;            // padded extents of the output (kToMaps)
   int nk, nseg;              // K blocks per segment; segment s multiplies parts pa[s], pb[s]
-  int chunk;                 // K blocks that one accumulator sums (see the kernel)
+  int head, chunk;           // K blocks of a tile's first accumulator and of the later ones
   int pa[3], pb[3];
   float f0, d0, f1, d1;      // output o: acc * f + (i == j) * d
   int has1, lo;              // a second output; both outputs in two parts
@@ -148,14 +149,30 @@ __device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, Ctl c
   }
 }
 
+// Four 8 x 8 blocks of 16-bit values: transposed out of shared memory, and back into it.
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
 // One 32-row x 64-column piece of a warp to the fp16 maps: both outputs, both parts, and the
 // mirrored piece of an off-diagonal tile. The warp's 8 KB stage is two halves that alternate, so
-// a piece is packed while the previous one's copy still reads its half.
+// a piece is packed while the previous one's copy still reads its half. A piece lies in its
+// half in the 128-byte swizzle (16-byte unit u of row i at u ^ (i & 7)); the mirrored piece is
+// read from there by transposing 8 x 8 blocks and lies in the 64-byte swizzle (unit u of row j at
+// u ^ (j / 2 & 3)): neither side has bank conflicts.
 __device__ __forceinline__ void emit_maps(const Prod& p, const CUtensorMap* out0,
                                           const CUtensorMap* out1, const CUtensorMap* mir0,
-                                          const CUtensorMap* mir1,
-                                          const float* v, int g, int row0, int col0,
-                                          bool mirror, uint8_t* stage, int lane, int& chunk) {
+                                          const CUtensorMap* mir1, const float* v, int g, int row0,
+                                          int col0, bool mirror, uint32_t stage, int lane,
+                                          int& chunk) {
 #pragma unroll 1
   for (int o = 0; o <= p.has1; ++o) {
     const float f = o ? p.f1 : p.f0, d = o ? p.d1 : p.d0;
@@ -163,46 +180,55 @@ __device__ __forceinline__ void emit_maps(const Prod& p, const CUtensorMap* out0
     for (int part = 0; part <= p.lo; ++part) {
       int dq = row0 + lane - col0;            // the diagonal's column of this row's 64
       asm volatile("" : "+r"(dq));            // (not 64 comparisons kept over the loops)
-      uint32_t h[32];
-#pragma unroll
-      for (int q = 0; q < 32; ++q) {
-        float a = v[2 * q] * f + (dq == 2 * q ? d : 0.f);
-        float b = v[2 * q + 1] * f + (dq == 2 * q + 1 ? d : 0.f);
-        __half2 w = __floats2half2_rn(a, b);
-        if (part) w = __floats2half2_rn(a - __low2float(w), b - __high2float(w));
-        h[q] = *reinterpret_cast<uint32_t*>(&w);
-      }
       const int z = part * p.batch + g;
-      uint8_t* half = stage + (chunk & 1) * 4096;
+      const uint32_t half = stage + (chunk & 1) * 4096;
       if (lane == 0) bulk_wait_read<1>();
       __syncwarp();
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        *reinterpret_cast<uint4*>(half + lane * 128 + ((u ^ (lane & 7)) << 4)) =
-            make_uint4(h[4 * u], h[4 * u + 1], h[4 * u + 2], h[4 * u + 3]);
+      for (int u = 0; u < 8; ++u) {
+        uint32_t h[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c = 8 * u + 2 * q;
+          const float a = v[c] * f + (dq == c ? d : 0.f);
+          const float b = v[c + 1] * f + (dq == c + 1 ? d : 0.f);
+          __half2 w = __floats2half2_rn(a, b);
+          if (part) w = __floats2half2_rn(a - __low2float(w), b - __high2float(w));
+          h[q] = *reinterpret_cast<uint32_t*>(&w);
+        }
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                         half + lane * 128 + ((u ^ (lane & 7)) << 4)),
+                     "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                     : "memory");
+      }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
-        store_box(o ? out1 : out0, smem_u32(half), col0, row0, z);
+        store_box(o ? out1 : out0, half, col0, row0, z);
         bulk_commit();
       }
       ++chunk;
       if (mirror) {
-        half = stage + (chunk & 1) * 4096;
+        const uint32_t other = stage + (chunk & 1) * 4096;
         if (lane == 0) bulk_wait_read<1>();
         __syncwarp();
         const uint32_t flip = p.mirror < 0.f ? 0x80008000u : 0u;
-        uint16_t* col = reinterpret_cast<uint16_t*>(half) + lane;   // row j: 32 values of i
+        // lane l names row l of the piece's 32 for the load, and for the store row l % 8 of the
+        // unit's eight in 16-byte unit l / 8
+        const uint32_t src = half + lane * 128;
+        const int blk = lane >> 3, jj = lane & 7;
 #pragma unroll
-        for (int q = 0; q < 32; ++q) {
-          const uint32_t w = h[q] ^ flip;
-          col[(2 * q) * 32] = (uint16_t)w;
-          col[(2 * q + 1) * 32] = (uint16_t)(w >> 16);
+        for (int u = 0; u < 8; ++u) {
+          uint32_t r[4];
+          ldmatrix4_trans(src + ((u ^ (lane & 7)) << 4), r);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) r[q] ^= flip;
+          stmatrix4(other + (8 * u + jj) * 64 + ((blk ^ ((jj >> 1) & 3)) << 4), r);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          store_box(o ? mir1 : mir0, smem_u32(half), row0, col0, z);
+          store_box(o ? mir1 : mir0, other, row0, col0, z);
           bulk_commit();
         }
         ++chunk;
@@ -299,10 +325,8 @@ __device__ __forceinline__ void emit_user(const Prod& p, const float* v, int g, 
 // The tensor core adds to its fp32 accumulator without rounding to nearest: every 16-deep step
 // loses up to a whole unit in the last place, always towards zero, and K = 2048 in three
 // passes came out 3.8e-5 off. So the parts' small products (hi lo, lo hi) come first, and for fp32
-// results an accumulator sums only p.chunk K blocks; the epilogue warps add the accumulators
-// in registers (round to nearest) while the next one fills: 128 x 256 sums of a CTA are 128
-// registers of eight warps, and emptying one takes a quarter of the time that 256 deep take to
-// compute.
+// results an accumulator of large products sums only kChunk K blocks; the epilogue warps add the
+// accumulators in registers (round to nearest) while the next one fills.
 // Every wait is bounded; on expiry the device error word is set, the roles leave their loops,
 // copies and MMAs in flight are waited for (bounded) and TMEM is freed.
 template <int CG, bool B_MN>
@@ -333,7 +357,7 @@ ns_product_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_consta
   const bool leader = rank == 0;
   const Ctl ctl{abort_flag, p.err};
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
-  const int nk = p.nk * p.nseg;
+  const int nk = p.nk * p.nseg;   // K blocks of a tile: p.head, then p.chunk at a time
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -377,32 +401,35 @@ ns_product_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_consta
     if (warp == 0) {
       // ------------------------------------------------------------ TMA producer
       if (lane == 0) {
-        int it = 0;
+        int it = 0, s = 0;        // K blocks issued; ring slot and its phase
+        uint32_t ph = 1u;
         bool ok = true;
+        uint32_t fb0 = smem_u32(full);
+        if constexpr (CG == 2) fb0 = map_to_rank(fb0, 0);
         for (int tile = first; ok && tile < p.total; tile += step) {
           const Tile t = decode(p, tile);
           const int am = t.mb * TILE + (int)rank * 128, bn = t.nb * TILE + (int)rank * 128;
-          for (int kb = 0; kb < nk; ++kb, ++it) {
-            const int s = it % kStages;
-            // stops only when the wait runs out: both CTAs of a pair are released by the same
-            // commits, so both have then issued the same loads
-            if (!wait_inline(smem_u32(empty + s), ((uint32_t)(it / kStages) & 1u) ^ 1u, ctl,
-                             kErrProducer, kWaitLimitNs, /*stop_on_abort=*/false)) {
-              ok = false;
-              break;
-            }
-            const int seg = kb / p.nk, k = (kb - seg * p.nk) * BK;
+          for (int seg = 0; ok && seg < p.nseg; ++seg) {
             const int za = p.pa[seg] * p.batch + t.g, zb = p.pb[seg] * p.batch + t.g;
-            uint32_t fb = smem_u32(full + s);
-            if (leader) mbar_expect_tx(fb, CG * 2 * kPartBytes);
-            if constexpr (CG == 2) fb = map_to_rank(fb, 0);
-            load_box<CG>(smem_u32(sa + s * kPartBytes), &tma_a, fb, k, am, za);
-            const uint32_t db = smem_u32(sb + s * kPartBytes);
-            if constexpr (B_MN) {
-              load_box<CG>(db, &tma_b, fb, bn, k, zb);
-              load_box<CG>(db + 64 * BK * 2, &tma_b, fb, bn + 64, k, zb);
-            } else {
-              load_box<CG>(db, &tma_b, fb, k, bn, zb);
+            for (int k = 0; k < p.nk * BK; k += BK, ++it) {
+              // stops only when the wait runs out: both CTAs of a pair are released by the same
+              // commits, so both have then issued the same loads
+              if (!wait_inline(smem_u32(empty + s), ph, ctl, kErrProducer, kWaitLimitNs,
+                               /*stop_on_abort=*/false)) {
+                ok = false;
+                break;
+              }
+              const uint32_t fb = fb0 + (uint32_t)(s * 8);
+              if (leader) mbar_expect_tx(smem_u32(full + s), CG * 2 * kPartBytes);
+              load_box<CG>(smem_u32(sa + s * kPartBytes), &tma_a, fb, k, am, za);
+              const uint32_t db = smem_u32(sb + s * kPartBytes);
+              if constexpr (B_MN) {
+                load_box<CG>(db, &tma_b, fb, bn, k, zb);
+                load_box<CG>(db + 64 * BK * 2, &tma_b, fb, bn + 64, k, zb);
+              } else {
+                load_box<CG>(db, &tma_b, fb, k, bn, zb);
+              }
+              if (++s == kStages) { s = 0; ph ^= 1u; }
             }
           }
         }
@@ -420,36 +447,36 @@ ns_product_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_consta
           if constexpr (CG == 2) umma_commit_pair_both(bar);
           else umma_commit(bar);
         };
-        int it = 0, count = 0;   // K blocks, accumulators
+        int s = 0, count = 0;   // ring slot, accumulators used
+        uint32_t ph = 0u;
         bool ok = true;
         for (int tile = first; ok && tile < p.total; tile += step) {
-          for (int kb0 = 0; ok && kb0 < nk; kb0 += p.chunk, ++count) {
-            const int acc = count & 1, kb1 = min(nk, kb0 + p.chunk);
-            if (!wait_inline(smem_u32(tempty + acc), ((uint32_t)(count >> 1) & 1u) ^ 1u, ctl, kErrMma,
-                              kWaitLimitNs)) {
+          for (int kb = 0, end = p.head; ok && kb < nk; end = min(nk, end + p.chunk), ++count) {
+            const int acc = count & 1;
+            if (!wait_inline(smem_u32(tempty + acc), ((uint32_t)(count >> 1) & 1u) ^ 1u, ctl,
+                             kErrMma)) {
               ok = false;
               break;
             }
             tc_fence_after();
             const uint32_t d = tmem_base + (uint32_t)(acc * TILE);
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-              const int s = it % kStages;
-              if (!wait_inline(smem_u32(full + s), (uint32_t)(it / kStages) & 1u, ctl, kErrMma,
-                                kWaitLimitNs)) {
+            for (uint32_t more = 0u; kb < end; ++kb) {
+              if (!wait_inline(smem_u32(full + s), ph, ctl, kErrMma)) {
                 ok = false;
                 break;
               }
               tc_fence_after();
               const uint32_t a0 = smem_u32(sa + s * kPartBytes), b0 = smem_u32(sb + s * kPartBytes);
 #pragma unroll
-              for (int kk = 0; kk < BK / 16; ++kk) {
+              for (int kk = 0; kk < BK / 16; ++kk, more = 1u) {
                 const uint64_t ad = smem_desc(a0 + kk * 32, 16, 1024);
                 const uint64_t bd = B_MN ? smem_desc(b0 + kk * 2048, 64 * BK * 2, 1024)
                                          : smem_desc(b0 + kk * 32, 16, 1024);
-                if constexpr (CG == 2) umma_bf16_pair(d, ad, bd, id, (kb > kb0 || kk > 0) ? 1u : 0u);
-                else umma_bf16(d, ad, bd, id, (kb > kb0 || kk > 0) ? 1u : 0u);
+                if constexpr (CG == 2) umma_bf16_pair(d, ad, bd, id, more);
+                else umma_bf16(d, ad, bd, id, more);
               }
               commit(smem_u32(empty + s));
+              if (++s == kStages) { s = 0; ph ^= 1u; }
             }
             if (ok) commit(smem_u32(tfull + acc));
           }
@@ -477,7 +504,7 @@ ns_product_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_consta
       float v[COLS];
 #pragma unroll
       for (int q = 0; q < COLS; ++q) v[q] = 0.f;
-      for (int kb0 = 0; kb0 < nk; kb0 += p.chunk, ++count) {
+      for (int done = 0; done < nk; done = done ? done + p.chunk : p.head, ++count) {
         const int acc = count & 1;
         if (!wait_inline(smem_u32(tfull + acc), (uint32_t)(count >> 1) & 1u, ctl, kErrEpilogue)) {
           ok = false;
@@ -509,7 +536,8 @@ ns_product_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_consta
         const int col0 = t.nb * TILE + cbase + c;
         if (row0 >= rmax || col0 >= cmax || (p.fmode == kPacked && col0 + 63 <= row0)) continue;
         if (p.fmode == kToMaps)
-          emit_maps(p, &out0, &out1, &mir0, &mir1, v + c, t.g, row0, col0, mirror, stage, lane, chunk);
+          emit_maps(p, &out0, &out1, &mir0, &mir1, v + c, t.g, row0, col0, mirror,
+                    smem_u32(stage), lane, chunk);
         else
           emit_user(p, v + c, t.g, row0, col0, stage, lane);
       }
@@ -661,7 +689,7 @@ __global__ void __launch_bounds__(256) ns_prep_kernel(const __grid_constant__ Pr
 // ------------------------------------------------------------------ host side
 // fp16 stack [mats][rows][cols], box {bx, by, 1}
 bool make_map3(CUtensorMap* m, const void* base, int64_t mats, int64_t rows, int64_t cols, int bx,
-               int by, bool swizzle) {
+               int by, CUtensorMapSwizzle swizzle) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)mats};
@@ -670,8 +698,7 @@ bool make_map3(CUtensorMap* m, const void* base, int64_t mats, int64_t rows, int
   cuuint32_t estr[3] = {1u, 1u, 1u};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // A workspace stack and the ways the products address it.
@@ -681,8 +708,11 @@ struct Stack {
   CUtensorMap k, mn, st, mir;   // K-major operand, N-major operand, store, mirrored store
   bool init(__half* b, int64_t mats, int64_t r, int64_t c) {
     base = b; rows = r; cols = c;
-    return make_map3(&k, b, mats, r, c, 64, 128, true) && make_map3(&mn, b, mats, r, c, 64, 64, true) &&
-           make_map3(&st, b, mats, r, c, 64, 32, true) && make_map3(&mir, b, mats, r, c, 32, 64, false);
+    constexpr CUtensorMapSwizzle k128 = CU_TENSOR_MAP_SWIZZLE_128B, k64 = CU_TENSOR_MAP_SWIZZLE_64B;
+    return make_map3(&k, b, mats, r, c, 64, 128, k128) &&
+           make_map3(&mn, b, mats, r, c, 64, 64, k128) &&
+           make_map3(&st, b, mats, r, c, 64, 32, k128) &&
+           make_map3(&mir, b, mats, r, c, 32, 64, k64);
   }
 };
 
@@ -857,7 +887,9 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
     q.total = (int)tiles(rows, cols, tile, sym);
     q.rows = (int)rows; q.cols = (int)cols;
     q.nk = (int)(K / BK);
-    q.chunk = exact ? 4 : q.nk * q.nseg;
+    // the small products and the first of the large ones in one accumulator
+    q.head = exact ? (q.nseg - 1) * q.nk + std::min(kChunk, q.nk) : q.nk * q.nseg;
+    q.chunk = kChunk;
     q.err = err;
     if (b_mn)
       return pair ? launch<2, true>(a, b, o0, o1, q, sms, name, s)
