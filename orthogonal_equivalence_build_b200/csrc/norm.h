@@ -24,6 +24,7 @@ struct Bwd {
   float *dgamma, *dbeta;      // [m] or NULL
   float* part;                // [2][parts][m]: column sums per range of rows
   int parts;
+  int* err;                   // device error word (bounded waits)
 };
 
 size_t bwd_ws_bytes(int64_t T, int64_t m);
