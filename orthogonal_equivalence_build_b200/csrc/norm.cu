@@ -143,18 +143,18 @@ __global__ void __launch_bounds__(kThreads) ln_cols_any_kernel(const Bwd a) {
   }
 }
 
-// dgamma and dbeta: the ranges' sums, 32 columns per block; eight threads of a column take every
-// eighth range, and their sums are added in order.
-__global__ void __launch_bounds__(kThreads) ln_cols_sum_kernel(const Bwd a) {
-  __shared__ float sg[8][33], sb[8][33];
+// dgamma and dbeta: the ranges' sums, 32 columns per block; 32 threads of a column take every 32nd
+// range, and their sums are added by a fixed tree.
+__global__ void __launch_bounds__(1024) ln_cols_sum_kernel(const Bwd a) {
+  __shared__ float sg[32][33], sb[32][33];
   pdl_wait();
   pdl_trigger();
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + tx;
   float g = 0.f, b = 0.f;
   if (c < a.m) {
-#pragma unroll 4
-    for (int p = ty; p < a.parts; p += 8) {
+#pragma unroll 5
+    for (int p = ty; p < a.parts; p += 32) {
       g += a.part[(int64_t)p * a.m + c];
       b += a.part[((int64_t)a.parts + p) * a.m + c];
     }
@@ -162,13 +162,18 @@ __global__ void __launch_bounds__(kThreads) ln_cols_sum_kernel(const Bwd a) {
   sg[ty][tx] = g;
   sb[ty][tx] = b;
   __syncthreads();
-  if (ty == 0 && c < a.m) {
-    for (int k = 1; k < 8; ++k) {
-      g += sg[k][tx];
-      b += sb[k][tx];
-    }
-    if (a.dgamma) a.dgamma[c] = g;
-    if (a.dbeta) a.dbeta[c] = b;
+  // warp w adds column w's 32 sums
+  g = sg[tx][ty];
+  b = sb[tx][ty];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    g += __shfl_xor_sync(0xffffffffu, g, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  const int64_t col = (int64_t)blockIdx.x * 32 + ty;
+  if (tx == 0 && col < a.m) {
+    if (a.dgamma) a.dgamma[col] = g;
+    if (a.dbeta) a.dbeta[col] = b;
   }
 }
 
@@ -214,93 +219,91 @@ __device__ __forceinline__ void stv(T* p, const float (&f)[V]) {
     *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
   }
 }
-// V weights of either type
-template <int V>
-__device__ __forceinline__ void ldw(const void* w, int w_bf16, int64_t i, float none,
-                                    float (&f)[V]) {
-  if (!w) {
+// V weights of type WT at p (NULL: `none`)
+template <typename WT, int V>
+__device__ __forceinline__ void ldw(const WT* p, int i, float none, float (&f)[V]) {
+  if constexpr (V == 1) {
+    f[0] = p ? ld(p, i) : none;
+  } else {
 #pragma unroll
     for (int k = 0; k < V; ++k) f[k] = none;
-  } else if (w_bf16) {
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(w) + i;
-    if constexpr (V == 8) {
-      Vec<__nv_bfloat16, 8> v;
-      v.load(p);
-      v.get(f);
-    } else if constexpr (V == 4) {
-      const uint2 u = *reinterpret_cast<const uint2*>(p);
-      f[0] = __uint_as_float(u.x << 16); f[1] = __uint_as_float(u.x & 0xffff0000u);
-      f[2] = __uint_as_float(u.y << 16); f[3] = __uint_as_float(u.y & 0xffff0000u);
-    } else {
-      f[0] = ld(p, 0);
-    }
-  } else {
-    const float* p = static_cast<const float*>(w) + i;
-    if constexpr (V == 1) {
-      f[0] = *p;
-    } else {
+    if (p) {
+      if constexpr (sizeof(WT) == 4) {
 #pragma unroll
-      for (int k = 0; k < V; k += 4) {
-        const float4 a = *reinterpret_cast<const float4*>(p + k);
-        f[k] = a.x; f[k + 1] = a.y; f[k + 2] = a.z; f[k + 3] = a.w;
+        for (int k = 0; k < V; k += 4) {
+          const float4 a = *reinterpret_cast<const float4*>(p + i + k);
+          f[k] = a.x; f[k + 1] = a.y; f[k + 2] = a.z; f[k + 3] = a.w;
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < V; k += 4) {
+          const uint2 u = *reinterpret_cast<const uint2*>(p + i + k);
+          f[k] = __uint_as_float(u.x << 16); f[k + 1] = __uint_as_float(u.x & 0xffff0000u);
+          f[k + 2] = __uint_as_float(u.y << 16); f[k + 3] = __uint_as_float(u.y & 0xffff0000u);
+        }
       }
     }
   }
 }
 
-// Sums of a and b over the threads of one row: blockDim.x threads (whole warps), row threadIdx.y of
-// the block. `buf` holds a float2 per warp of the block; two calls in a row take different ones, so
-// one barrier each is enough.
-__device__ __forceinline__ float2 row_sum(float a, float b, float2* buf) {
+// Sums of a and b over the W warps of one row (row threadIdx.y of the block). Two calls in a row
+// take different buffers, so one barrier each is enough.
+template <int W>
+__device__ __forceinline__ float2 row_sum(float a, float b, float2 (*buf)[W]) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     a += __shfl_xor_sync(0xffffffffu, a, o);
     b += __shfl_xor_sync(0xffffffffu, b, o);
   }
-  const int warps = blockDim.x >> 5;
-  if (warps == 1) return make_float2(a, b);
-  float2* mine = buf + threadIdx.y * warps;
+  if constexpr (W == 1) return make_float2(a, b);
+  float2* mine = buf[threadIdx.y];
   if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = make_float2(a, b);
   __syncthreads();
   float2 s = make_float2(0.f, 0.f);
-  for (int w = 0; w < warps; ++w) {
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
     s.x += mine[w].x;
     s.y += mine[w].y;
   }
   return s;
 }
 
-// Forward: blockDim.x threads hold a row, V x NV elements each; blockDim.y rows per block, one
-// block per group of rows. Many small blocks per SM keep enough rows in flight; a row is read
-// once and stays in registers over its two sums.
-template <typename T, int V, int NV>
-__global__ void __launch_bounds__(512) ln_fwd_kernel(const Fwd a) {
-  __shared__ float2 buf[2][16];
+// Forward: W warps hold a row, E elements per lane, packed as they came; blockDim.y rows per block.
+// A row is read once and stays in registers over its two sums. What bounds it is instructions as
+// much as bytes: everything that a row costs apart from its elements (two reductions, addresses,
+// statistics) is paid per lane, so long rows go to few lanes. 16384 x 4096 bf16: 128 threads a
+// row with 32 elements each 67 us, two blocks of 512 threads over a ring with 8 elements each
+// 94 us (37 instructions an element), one warp with 128 elements 46 us.
+template <typename T, typename WT, int V, int E, int W>
+__global__ void __launch_bounds__(W > 4 ? 32 * W : 128) ln_fwd_kernel(const Fwd a) {
+  constexpr int NV = E / V, ROWS = W > 4 ? 1 : 4 / W;
+  __shared__ float2 buf[2][ROWS][W];
   pdl_wait();
   pdl_trigger();
-  const int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.y;
   const int m = r < a.T ? (int)a.m : 0;   // a row past the last one has no elements
-  const T* x = static_cast<const T*>(a.x) + r * a.m;
+  const int c0 = threadIdx.x * V;         // vector i of a lane: column c0 + 32 W V i
+  const T* x = static_cast<const T*>(a.x) + r * a.m + c0;
   Vec<T, V> v[NV];
-  float f[V], s = 0.f;
+  float f[V];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (c0 + 32 * W * V * i < m) v[i].load(x + 32 * W * V * i);
+  float s = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * blockDim.x + threadIdx.x) * V;
-    if (c < m) v[i].load(x + c);
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if ((i * blockDim.x + threadIdx.x) * V < m) {
+    if (c0 + 32 * W * V * i < m) {
       v[i].get(f);
 #pragma unroll
       for (int k = 0; k < V; ++k) s += f[k];
     }
   }
-  const float mean = row_sum(s, 0.f, buf[0]).x / (float)a.m;
+  const float inv_m = 1.f / (float)a.m;
+  const float mean = row_sum<W>(s, 0.f, buf[0]).x * inv_m;
   float s1 = 0.f, s2 = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    if ((i * blockDim.x + threadIdx.x) * V < m) {
+    if (c0 + 32 * W * V * i < m) {
       v[i].get(f);
 #pragma unroll
       for (int k = 0; k < V; ++k) {
@@ -310,21 +313,23 @@ __global__ void __launch_bounds__(512) ln_fwd_kernel(const Fwd a) {
       }
     }
   }
-  const float2 d = row_sum(s1, s2, buf[1]);
-  const float dm = d.x / (float)a.m;
-  const float rstd = rstd_of(d.y / (float)a.m - dm * dm, a.eps);
-  T* y = static_cast<T*>(a.y) + r * a.m;
+  const float2 d = row_sum<W>(s1, s2, buf[1]);
+  const float dm = d.x * inv_m;
+  const float rstd = rstd_of(d.y * inv_m - dm * dm, a.eps);
+  T* y = static_cast<T*>(a.y) + r * a.m + c0;
+  const WT* gamma = static_cast<const WT*>(a.gamma);
+  const WT* beta = static_cast<const WT*>(a.beta);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * blockDim.x + threadIdx.x) * V;
+    const int c = c0 + 32 * W * V * i;
     if (c < m) {
       float g[V], b[V];
-      ldw<V>(a.gamma, a.w_bf16, c, 1.f, g);
-      ldw<V>(a.beta, a.w_bf16, c, 0.f, b);
+      ldw<WT, V>(gamma, c, 1.f, g);
+      ldw<WT, V>(beta, c, 0.f, b);
       v[i].get(f);
 #pragma unroll
       for (int k = 0; k < V; ++k) g[k] = (f[k] - mean - dm) * rstd * g[k] + b[k];
-      stv<T, V>(y + c, g);
+      stv<T, V>(y + 32 * W * V * i, g);
     }
   }
   if (threadIdx.x == 0 && m) {
@@ -333,39 +338,44 @@ __global__ void __launch_bounds__(512) ln_fwd_kernel(const Fwd a) {
   }
 }
 
-// Threads per row and rows per block of a width: V x NV elements per thread, whole warps.
-struct RowShape {
-  int threads, rows;
-};
-RowShape row_shape(int64_t m, int per_thread, int block) {
-  const int warps = (int)((m + 32 * per_thread - 1) / (32 * per_thread));
-  return {32 * warps, std::max(1, block / (32 * warps))};
-}
+constexpr int64_t kRegWidth = 16384;   // 16 warps x 32 lanes x 32 elements
 
-constexpr int64_t kRegWidth = 16384;   // 512 threads x 32 elements
-
-template <typename T, int V, int NV>
+template <typename T, typename WT, int V, int E, int W>
 cudaError_t launch_fwd(const Fwd& a, cudaStream_t s) {
-  const RowShape sh = row_shape(a.m, V * NV, 128);
-  const int64_t blocks = (a.T + sh.rows - 1) / sh.rows;
-  return launch_k(ln_fwd_kernel<T, V, NV>, dim3((unsigned)blocks),
-                  dim3((unsigned)sh.threads, (unsigned)sh.rows), 0, s, a);
+  constexpr int ROWS = W > 4 ? 1 : 4 / W;
+  return launch_k(ln_fwd_kernel<T, WT, V, E, W>, dim3((unsigned)((a.T + ROWS - 1) / ROWS)),
+                  dim3(32 * W, ROWS), 0, s, a);
 }
-// Elements per thread: few for short rows (a warp holds up to 256 with 8), 32 for long ones.
-template <typename T, int V>
+// E elements per lane and as few warps as hold the row
+template <typename T, typename WT, int V, int E>
+cudaError_t fwd_warps(const Fwd& a, cudaStream_t s) {
+  if (a.m <= 32 * E) return launch_fwd<T, WT, V, E, 1>(a, s);
+  if (a.m <= 64 * E) return launch_fwd<T, WT, V, E, 2>(a, s);
+  if (a.m <= 128 * E) return launch_fwd<T, WT, V, E, 4>(a, s);
+  if constexpr (E < 128) {
+    if (a.m <= 256 * E) return launch_fwd<T, WT, V, E, 8>(a, s);
+    if constexpr (E < 64) return launch_fwd<T, WT, V, E, 16>(a, s);
+  }
+  return cudaErrorInvalidValue;
+}
+// E: 8 where a warp then holds the row; as much as 64 registers hold (128 bf16, 64 fp32 values)
+// where there are rows enough to fill the GPU that way; 32 otherwise (few rows: more lanes, less
+// latency) and for rows that do not start on 16 bytes (a register per value).
+template <typename T, typename WT, int V>
 cudaError_t fwd_width(const Fwd& a, cudaStream_t s) {
-  if (a.m <= 256) return launch_fwd<T, V, 8 / V>(a, s);
-  if (a.m <= 1024) return launch_fwd<T, V, 16 / V>(a, s);
-  return launch_fwd<T, V, 32 / V>(a, s);
+  constexpr int kMost = V == 1 ? 32 : 256 / (int)sizeof(T);
+  if (a.m <= 256) return launch_fwd<T, WT, V, 8, 1>(a, s);
+  if constexpr (kMost > 32)
+    if (a.m > 1024 && a.T * ((a.m + 32 * kMost - 1) / (32 * kMost)) >= 8 * 148)
+      return fwd_warps<T, WT, V, kMost>(a, s);
+  return fwd_warps<T, WT, V, 32>(a, s);
 }
 
-// ------------------------------------------------------------------ backward, one pass
-// A persistent block takes groups of blockDim.y consecutive rows (blockDim.x threads each). The rows
-// of x and dy come through a ring of shared-memory slots by bulk copies, several groups ahead, so
-// that bytes are in flight whatever the block waits for; per group there is one barrier, which
-// completes the row sums and frees the slot. dx leaves from registers; a thread's columns are the
-// same in every row, so its shares of dgamma and dbeta stay in registers to the end, are added over
-// the block's rows at a time in shared memory and written once per block.
+// ------------------------------------------------------------------ rows through a ring
+// A persistent block takes groups of blockDim.y consecutive rows (blockDim.x threads each). The
+// rows come through a ring of shared-memory slots by bulk copies, groups ahead, so that bytes are
+// in flight whatever the block waits for. Elements are worked on in pairs (fp32 x 2
+// instructions): at bf16's two bytes an element, instructions count as much as bytes.
 // Rows that do not start on 16 bytes (V = 1) are copied as the 16-byte window around them.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar) {
@@ -375,204 +385,276 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       "l"(src), "r"(bytes), "r"(bar)
       : "memory");
 }
-// Bounded waits: on expiry the device error word is set and the block leaves.
-__device__ __forceinline__ bool wait_full(uint32_t bar, uint32_t parity, umma::Ctl c) {
-  return umma::wait_bounded(bar, parity, c, umma::kErrProducer, umma::kWaitLimitNs);
-}
-__device__ __forceinline__ void drain_full(uint32_t bar, uint32_t parity, umma::Ctl c) {
-  umma::wait_bounded(bar, parity, c, 0, umma::kDrainLimitNs, /*stop_on_abort=*/false);
-}
 
-constexpr int kRingBytes = 192 * 1024;
+constexpr int kRingBytes = 192 * 1024;   // per SM
 constexpr int kMaxStages = 6;
-constexpr int kMaxParts = 148;                   // one block per SM
 
-struct Ring {
-  int stages, slot;                              // slot: bytes of one group of x (and of dy)
+struct RingShape {
+  int stages, slot;                      // slot: bytes of one group of one array
 };
 
-template <typename T, int V, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1) ln_bwd_kernel(const Bwd a, const Ring ring) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t full[kMaxStages];
-  __shared__ float2 buf[2][MAXT / 32];
-  __shared__ int abort_flag;
-  const int m = (int)a.m, rows = blockDim.y;
-  const int tid = threadIdx.y * blockDim.x + threadIdx.x;
-  const int64_t groups = (a.T + rows - 1) / rows;
-  const umma::Ctl ctl{&abort_flag, a.err};
-  if (tid == 0) {
-    abort_flag = 0;
-    for (int s = 0; s < ring.stages; ++s) umma::mbar_init(umma::smem_u32(full + s), 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  }
-  __syncthreads();
-  pdl_wait();
-  pdl_trigger();
+// The ring of a block that reads ARR arrays [T][m] of one layout. All threads of the block make the
+// same calls; thread 0 issues the copies. Waits are bounded: on expiry the device error word is
+// set, wait() returns false and the block leaves through drain().
+template <typename T, int V, int ARR>
+struct Ring {
+  const char* src[ARR];
+  uint8_t* smem;
+  uint64_t* full;
+  umma::Ctl ctl;
+  RingShape sh;
+  int64_t row_bytes, total, groups, next;
+  int rows, s, used;
+  uint32_t ph;
 
-  // bytes of a group: [lo, hi) of the array, copied as [lo & ~15, end)
-  const int64_t row_bytes = (int64_t)m * sizeof(T), total = a.T * row_bytes;
-  auto window = [&](int64_t g, int64_t& from, int64_t& end, int64_t& hi) {
-    const int64_t lo = g * rows * row_bytes;
+  __device__ __forceinline__ int tid() const { return threadIdx.y * blockDim.x + threadIdx.x; }
+  // bytes of group g: [lo, hi) of the arrays, copied as [from, end)
+  __device__ __forceinline__ void window(int64_t g, int64_t& lo, int64_t& hi, int64_t& from,
+                                         int64_t& end) const {
+    lo = g * rows * row_bytes;
     hi = min(total, lo + rows * row_bytes);
     from = lo & ~(int64_t)15;
     end = min((hi + 15) & ~(int64_t)15, total & ~(int64_t)15);
     if (end < from) end = from;
-  };
-  auto fetch = [&](int64_t g, int s) {
-    int64_t from, end, hi;
-    window(g, from, end, hi);
-    const uint32_t bytes = (uint32_t)(end - from), bar = umma::smem_u32(full + s);
-    umma::mbar_expect_tx(bar, 2 * bytes);
+  }
+  __device__ __forceinline__ void fetch(int64_t g, int slot) const {
+    int64_t lo, hi, from, end;
+    window(g, lo, hi, from, end);
+    const uint32_t bytes = (uint32_t)(end - from), bar = umma::smem_u32(full + slot);
+    umma::mbar_expect_tx(bar, ARR * bytes);
     if (bytes) {
-      const uint32_t dst = umma::smem_u32(smem + (size_t)s * 2 * ring.slot);
-      bulk_load(dst, static_cast<const char*>(a.x) + from, bytes, bar);
-      bulk_load(dst + ring.slot, static_cast<const char*>(a.dy) + from, bytes, bar);
+#pragma unroll
+      for (int k = 0; k < ARR; ++k)
+        bulk_load(umma::smem_u32(smem + (size_t)(slot * ARR + k) * sh.slot), src[k] + from, bytes,
+                  bar);
     }
-  };
-  if (tid == 0)
-    for (int s = 0; s < ring.stages; ++s) {
-      const int64_t g = blockIdx.x + (int64_t)s * gridDim.x;
-      if (g < groups) fetch(g, s);
+  }
+  __device__ __forceinline__ void init(uint8_t* buf, uint64_t* bars, int* abort_flag, int* err,
+                                       RingShape shape, int64_t T_, int64_t m) {
+    smem = buf; full = bars; sh = shape; rows = blockDim.y;
+    ctl = umma::Ctl{abort_flag, err};
+    row_bytes = m * sizeof(T);
+    total = T_ * row_bytes;
+    groups = (T_ + rows - 1) / rows;
+    s = used = 0;
+    ph = 0;
+    if (tid() == 0) {
+      *abort_flag = 0;
+      for (int k = 0; k < sh.stages; ++k) umma::mbar_init(umma::smem_u32(full + k), 1);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
+    __syncthreads();
+  }
+  __device__ __forceinline__ void start() {
+    next = blockIdx.x;
+    for (int k = 0; k < sh.stages; ++k, next += gridDim.x)
+      if (tid() == 0 && next < groups) fetch(next, k);
+  }
+  // the current slot's row of this thread's group row, or false
+  __device__ __forceinline__ bool wait(int64_t g) {
+    const bool ok = umma::wait_bounded(umma::smem_u32(full + s), ph, ctl, umma::kErrProducer,
+                                       umma::kWaitLimitNs);
+    if constexpr (V == 1) {
+      // the arrays' last bytes, which no 16-byte copy inside them covers
+      int64_t lo, hi, from, end;
+      window(g, lo, hi, from, end);
+      if (end < hi) {
+        for (int64_t b = end + (int64_t)tid() * sizeof(T); b < hi;
+             b += (int64_t)blockDim.x * rows * sizeof(T))
+#pragma unroll
+          for (int k = 0; k < ARR; ++k)
+            *reinterpret_cast<T*>(smem + (size_t)(s * ARR + k) * sh.slot + (lo & 15) + (b - lo)) =
+                *reinterpret_cast<const T*>(src[k] + b);
+        __syncthreads();
+      }
+    }
+    return ok;
+  }
+  __device__ __forceinline__ const T* row(int64_t g, int k) const {
+    return reinterpret_cast<const T*>(smem + (size_t)(s * ARR + k) * sh.slot +
+                                      ((g * rows * row_bytes) & 15) + threadIdx.y * row_bytes);
+  }
+  // After the barrier of the current group: the slot of the group before it has been read by every
+  // thread and takes the next group to come; on to the next slot.
+  __device__ __forceinline__ void release() {
+    if (used++ > 0) {
+      if (tid() == 0 && next < groups) fetch(next, s == 0 ? sh.stages - 1 : s - 1);
+      next += gridDim.x;
+    }
+    if (++s == sh.stages) { s = 0; ph ^= 1u; }
+  }
+  // let the copies in flight land before the block leaves
+  __device__ __forceinline__ void drain() {
+    if (tid() == 0)
+      for (int k = 0; k < sh.stages; ++k) {
+        umma::wait_bounded(umma::smem_u32(full + s), ph, ctl, 0, umma::kDrainLimitNs,
+                           /*stop_on_abort=*/false);
+        if (++s == sh.stages) { s = 0; ph ^= 1u; }
+      }
+  }
+};
 
-  float ag[NV][V], ab[NV][V];
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Backward. dx leaves from the block; a thread's columns (32 of them: vector i starts at column
+// (i blockDim.x + threadIdx.x) V) are the same in every row, so its shares of dgamma and dbeta stay
+// in 64 registers to the end, are added over the block's rows in shared memory and written once per
+// block. Per group there is one barrier: it completes the row sums, and it frees the slot of the
+// group before, which was read for the last time since the previous barrier.
+template <typename T, typename WT, int V>
+__global__ void __launch_bounds__(512, 1) ln_bwd_ring_kernel(const Bwd a, const RingShape shape) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ float2 buf[2][16];
+  __shared__ int abort_flag;
+  constexpr int NV = 32 / V, P = V > 1 ? V / 2 : 1;
+  const int m = (int)a.m, warps = blockDim.x >> 5, step = blockDim.x * V;
+  Ring<T, V, 2> ring;
+  ring.src[0] = static_cast<const char*>(a.x);
+  ring.src[1] = static_cast<const char*>(a.dy);
+  ring.init(smem, full, &abort_flag, a.err, shape, a.T, a.m);
+  pdl_wait();
+  pdl_trigger();
+  ring.start();
+  const WT* gamma = static_cast<const WT*>(a.gamma);
+  const int c0 = threadIdx.x * V;
+  float ag[32], ab[32];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int k = 0; k < V; ++k) ag[i][k] = ab[i][k] = 0.f;
-  float mean_n = 0.f, rstd_n = 0.f;              // of the next group's row
+  for (int k = 0; k < 32; ++k) ag[k] = ab[k] = 0.f;
+  float mean_n = 0.f, rstd_n = 0.f;          // of the next group's row
   auto stats = [&](int64_t g) {
-    const int64_t r = g * rows + threadIdx.y;
+    const int64_t r = g * ring.rows + threadIdx.y;
     if (r < a.T) {
       mean_n = __ldg(a.mean + r);
       rstd_n = __ldg(a.rstd + r);
     }
   };
   stats(blockIdx.x);
-
-  int s = 0, turn = 0;
-  uint32_t ph = 0;
+  const float inv_m = 1.f / (float)m;
   bool bad = false;
-  int64_t issued = blockIdx.x + (int64_t)ring.stages * gridDim.x;   // next group to fetch
-  for (int64_t g = blockIdx.x; g < groups; g += gridDim.x) {
-    const int64_t r = g * rows + threadIdx.y;
+  int turn = 0;
+  for (int64_t g = blockIdx.x; g < ring.groups; g += gridDim.x) {
+    const int64_t r = g * ring.rows + threadIdx.y;
     const int live = r < a.T ? m : 0;
     const float mean = mean_n, rstd = rstd_n;
-    const bool ok = wait_full(umma::smem_u32(full + s), ph, ctl);
-    const int64_t lo = g * rows * row_bytes;
-    uint8_t* sx = smem + (size_t)s * 2 * ring.slot + (lo & 15);
-    if constexpr (V == 1) {
-      // the array's last bytes, which no 16-byte copy inside it covers
-      int64_t from, end, hi;
-      window(g, from, end, hi);
-      if (end < hi) {
-        for (int64_t b = end + (int64_t)tid * sizeof(T); b < hi;
-             b += (int64_t)blockDim.x * rows * sizeof(T)) {
-          *reinterpret_cast<T*>(sx + (b - lo)) =
-              *reinterpret_cast<const T*>(static_cast<const char*>(a.x) + b);
-          *reinterpret_cast<T*>(sx + ring.slot + (b - lo)) =
-              *reinterpret_cast<const T*>(static_cast<const char*>(a.dy) + b);
-        }
-        __syncthreads();
-      }
-    }
-    const T* px = reinterpret_cast<const T*>(sx) + threadIdx.y * m;
-    const T* pd = reinterpret_cast<const T*>(sx + ring.slot) + threadIdx.y * m;
-    Vec<T, V> vx[NV], vd[NV];
-    float s1 = 0.f, s2 = 0.f;
+    const bool ok = ring.wait(g);
+    const T* px = ring.row(g, 0) + c0;
+    const T* pd = ring.row(g, 1) + c0;
+    float2 s1 = both(0.f), s2 = both(0.f);
+    int c = c0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * V;
+    for (int i = 0; i < NV; ++i, c += step) {
       if (c < live) {
-        vx[i].load(px + c);
-        vd[i].load(pd + c);
+        Vec<T, V> vx, vd;
         float x[V], d[V], w[V];
-        vx[i].get(x);
-        vd[i].get(d);
-        ldw<V>(a.gamma, a.w_bf16, c, 1.f, w);
+        vx.load(px + i * step);
+        vd.load(pd + i * step);
+        vx.get(x);
+        vd.get(d);
+        ldw<WT, V>(gamma, c, 1.f, w);
+        if constexpr (V == 1) {
+          const float h = (x[0] - mean) * rstd, gk = d[0] * w[0];
+          ag[i] += d[0] * h;
+          ab[i] += d[0];
+          s1.x += gk;
+          s2.x += gk * h;
+        } else {
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const float xh = (x[k] - mean) * rstd, gk = d[k] * w[k];
-          ag[i][k] += d[k] * xh;
-          ab[i][k] += d[k];
-          s1 += gk;
-          s2 += gk * xh;
+          for (int k = 0; k < P; ++k) {
+            const float2 d2 = make_float2(d[2 * k], d[2 * k + 1]);
+            const float2 h = __fmul2_rn(
+                __fadd2_rn(make_float2(x[2 * k], x[2 * k + 1]), both(-mean)), both(rstd));
+            const float2 gk = __fmul2_rn(d2, make_float2(w[2 * k], w[2 * k + 1]));
+            float2* eg = reinterpret_cast<float2*>(ag + i * V) + k;
+            float2* eb = reinterpret_cast<float2*>(ab + i * V) + k;
+            *eg = __ffma2_rn(d2, h, *eg);
+            *eb = __fadd2_rn(*eb, d2);
+            s1 = __fadd2_rn(s1, gk);
+            s2 = __ffma2_rn(gk, h, s2);
+          }
         }
       }
     }
+    float2 t = make_float2(s1.x + s1.y, s2.x + s2.y);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      s1 += __shfl_xor_sync(0xffffffffu, s1, o);
-      s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+      t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
+      t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
     }
-    const int warps = blockDim.x >> 5;
     float2* sums = buf[turn] + threadIdx.y * warps;   // (the other one may still be read)
     turn ^= 1;
-    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = make_float2(s1, s2);
-    if (g + gridDim.x < groups) stats(g + gridDim.x);
-    bad = __syncthreads_or(!ok);                 // the slot has been read by every thread
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = t;
+    if (g + gridDim.x < ring.groups) stats(g + gridDim.x);
+    bad = __syncthreads_or(!ok);
     if (bad) break;
-    if (tid == 0 && issued < groups) fetch(issued, s);
-    issued += gridDim.x;
-    if (warps > 1) {
-      s1 = s2 = 0.f;
-      for (int w = 0; w < warps; ++w) {
-        s1 += sums[w].x;
-        s2 += sums[w].y;
-      }
-    }
+    ring.release();
     if (a.dx) {
-      const float c1 = s1 / (float)m, c2 = s2 / (float)m;
-      T* dx = static_cast<T*>(a.dx) + r * m;
+      if (warps > 1) {
+        t = both(0.f);
+        for (int w = 0; w < warps; ++w) {
+          t.x += sums[w].x;
+          t.y += sums[w].y;
+        }
+      }
+      const float c1 = t.x * inv_m, c2 = t.y * inv_m;
+      T* dx = static_cast<T*>(a.dx) + r * a.m + c0;
+      c = c0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * V;
+      for (int i = 0; i < NV; ++i, c += step) {
         if (c < live) {
+          Vec<T, V> vx, vd;
           float x[V], d[V], w[V];
-          vx[i].get(x);
-          vd[i].get(d);
-          ldw<V>(a.gamma, a.w_bf16, c, 1.f, w);
+          vx.load(px + i * step);
+          vd.load(pd + i * step);
+          vx.get(x);
+          vd.get(d);
+          ldw<WT, V>(gamma, c, 1.f, w);
+          // rstd (g - c1 - xh c2)
+          if constexpr (V == 1) {
+            d[0] = rstd * (d[0] * w[0] - c1 - (x[0] - mean) * rstd * c2);
+          } else {
 #pragma unroll
-          for (int k = 0; k < V; ++k)
-            d[k] = rstd * (d[k] * w[k] - c1 - (x[k] - mean) * rstd * c2);
-          stv<T, V>(dx + c, d);
+            for (int k = 0; k < P; ++k) {
+              const float2 h = __fmul2_rn(
+                  __fadd2_rn(make_float2(x[2 * k], x[2 * k + 1]), both(-mean)), both(rstd));
+              float2 e = __ffma2_rn(make_float2(d[2 * k], d[2 * k + 1]),
+                                    make_float2(w[2 * k], w[2 * k + 1]), both(-c1));
+              e = __fmul2_rn(__ffma2_rn(h, both(-c2), e), both(rstd));
+              d[2 * k] = e.x;
+              d[2 * k + 1] = e.y;
+            }
+          }
+          stv<T, V>(dx + i * step, d);
         }
       }
     }
-    if (++s == ring.stages) { s = 0; ph ^= 1u; }
   }
   if (bad) {
-    // let the copies in flight land before the block leaves (its slots from s on, in ring order)
-    if (tid == 0)
-      for (int k = 0; k < ring.stages; ++k) {
-        drain_full(umma::smem_u32(full + s), ph, ctl);
-        if (++s == ring.stages) { s = 0; ph ^= 1u; }
-      }
+    ring.drain();
     return;
   }
   if (!a.part) return;
-  // the block's column sums, its rows at a time added in order; no copy is in flight any more
+  // the block's column sums, its rows added in order; no copy is in flight any more
   float* out_g = a.part + (int64_t)blockIdx.x * m;
   float* out_b = a.part + ((int64_t)gridDim.x + blockIdx.x) * m;
   float* sh = reinterpret_cast<float*>(smem);    // [rows][2][m]
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * blockDim.x + threadIdx.x) * V;
+    const int c = c0 + i * step;
     if (c < m) {
 #pragma unroll
       for (int k = 0; k < V; ++k) {
-        sh[(threadIdx.y * 2) * m + c + k] = ag[i][k];
-        sh[(threadIdx.y * 2 + 1) * m + c + k] = ab[i][k];
+        sh[(threadIdx.y * 2) * m + c + k] = ag[i * V + k];
+        sh[(threadIdx.y * 2 + 1) * m + c + k] = ab[i * V + k];
       }
     }
   }
   __syncthreads();
-  for (int c = tid; c < m; c += blockDim.x * rows) {
+  for (int c = ring.tid(); c < m; c += blockDim.x * blockDim.y) {
     float g = 0.f, b = 0.f;
-    for (int y = 0; y < rows; ++y) {
+    for (int y = 0; y < ring.rows; ++y) {
       g += sh[(y * 2) * m + c];
       b += sh[(y * 2 + 1) * m + c];
     }
@@ -581,29 +663,39 @@ __global__ void __launch_bounds__(MAXT, 1) ln_bwd_kernel(const Bwd a, const Ring
   }
 }
 
-// Shape of the one-pass kernel for a width, or stages < 2: too wide for the ring.
-struct BwdShape {
-  RowShape rows;
-  Ring ring;
+constexpr int kMaxParts = 148;   // one block per SM
+
+// Threads per row, rows per group and ring for a width; stages < 2: a row is too wide for the ring.
+// A group is at most 64 KB of x and dy (three slots in flight), and no larger than leaves a group
+// for every SM.
+struct GroupShape {
+  int threads, rows;
+  RingShape ring;
+  size_t smem;
 };
-BwdShape bwd_shape(int64_t m, int esz) {
-  BwdShape sh;
-  sh.rows = row_shape(m, 16, 512);
-  // x and dy of a group, the window's slack included; at the end the ring holds the column sums
-  sh.ring.slot = (int)(((int64_t)sh.rows.rows * m * esz + 15 + 16) / 16 * 16);
-  sh.ring.stages = (int)std::min<int64_t>(kMaxStages, kRingBytes / (2 * (int64_t)sh.ring.slot));
+GroupShape group_shape(int64_t T, int64_t m, int esz) {
+  GroupShape sh;
+  sh.threads = 32 * (int)((m + 1023) / 1024);   // 32 elements per thread
+  int64_t rows = std::min<int64_t>(512 / sh.threads, 64 * 1024 / (2 * m * esz));
+  rows = std::min<int64_t>(rows, (T + kMaxParts - 1) / kMaxParts);
+  sh.rows = (int)std::max<int64_t>(1, rows);
+  // the window around unaligned rows needs up to 30 bytes more
+  sh.ring.slot = (int)(((int64_t)sh.rows * m * esz + 31) / 16 * 16);
+  const int64_t stage = 2 * (int64_t)sh.ring.slot;
+  sh.ring.stages = (int)std::min<int64_t>(kMaxStages, kRingBytes / stage);
+  // at the end the ring's memory holds the block's column sums
+  sh.smem = std::max((size_t)(sh.ring.stages * stage), (size_t)sh.rows * 2 * m * sizeof(float));
   return sh;
 }
 
-template <typename T, int V, int MAXT>
-cudaError_t launch_bwd(const Bwd& a, const BwdShape& sh, int grid, cudaStream_t s) {
-  auto kern = ln_bwd_kernel<T, V, 16 / V, MAXT>;
-  const size_t smem = std::max((size_t)sh.ring.stages * 2 * sh.ring.slot,
-                               (size_t)sh.rows.rows * 2 * a.m * sizeof(float));
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <typename T, typename WT, int V>
+cudaError_t launch_bwd(const Bwd& a, const GroupShape& sh, cudaStream_t s) {
+  auto kern = ln_bwd_ring_kernel<T, WT, V>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem);
   if (e != cudaSuccess) return e;
-  return launch_k(kern, dim3((unsigned)grid), dim3((unsigned)sh.rows.threads, (unsigned)sh.rows.rows),
-                  smem, s, a, sh.ring);
+  return launch_k(kern, dim3((unsigned)a.parts), dim3((unsigned)sh.threads, (unsigned)sh.rows),
+                  sh.smem, s, a, sh.ring);
 }
 
 int row_blocks(int64_t T) { return (int)std::min<int64_t>(T, 148 * 8); }
@@ -618,14 +710,18 @@ size_t bwd_ws_bytes(int64_t T, int64_t m) {
 
 cudaError_t fwd(const Fwd& a, DT t, cudaStream_t s) {
   TraceScope tr("ln_fwd", s);
+  using bf16 = __nv_bfloat16;
   if (a.m <= kRegWidth && a.T < INT32_MAX) {
     const bool vec = a.m * (t == DT::BF16 ? 2 : 4) % 16 == 0;   // every row starts on 16 bytes
-    if (t == DT::BF16)
-      return vec ? fwd_width<__nv_bfloat16, 8>(a, s) : fwd_width<__nv_bfloat16, 1>(a, s);
-    return vec ? fwd_width<float, 4>(a, s) : fwd_width<float, 1>(a, s);
+    if (t == DT::BF16) {
+      if (vec) return a.w_bf16 ? fwd_width<bf16, bf16, 8>(a, s) : fwd_width<bf16, float, 8>(a, s);
+      return a.w_bf16 ? fwd_width<bf16, bf16, 1>(a, s) : fwd_width<bf16, float, 1>(a, s);
+    }
+    if (vec) return a.w_bf16 ? fwd_width<float, bf16, 4>(a, s) : fwd_width<float, float, 4>(a, s);
+    return a.w_bf16 ? fwd_width<float, bf16, 1>(a, s) : fwd_width<float, float, 1>(a, s);
   }
   const dim3 grid((unsigned)row_blocks(a.T)), block(kThreads);
-  return t == DT::BF16 ? launch_k(ln_fwd_any_kernel<__nv_bfloat16>, grid, block, 0, s, a)
+  return t == DT::BF16 ? launch_k(ln_fwd_any_kernel<bf16>, grid, block, 0, s, a)
                        : launch_k(ln_fwd_any_kernel<float>, grid, block, 0, s, a);
 }
 
@@ -638,32 +734,26 @@ cudaError_t bwd(Bwd a, DT t, void* ws, cudaStream_t s) {
   a.err = device_error_word();
   if (!a.err) return cudaErrorUnknown;
   cudaError_t e = cudaSuccess;
-  const BwdShape sh = a.m <= kRegWidth ? bwd_shape(a.m, esz) : BwdShape{};
+  const GroupShape sh = a.m <= kRegWidth ? group_shape(a.T, a.m, esz) : GroupShape{};
   if (a.m <= kRegWidth && sh.ring.stages >= 2) {
-    const int64_t groups = (a.T + sh.rows.rows - 1) / sh.rows.rows;
+    const int64_t groups = (a.T + sh.rows - 1) / sh.rows;
     a.parts = (int)std::min<int64_t>(groups, kMaxParts);
+    const bool vec = a.m * esz % 16 == 0;   // every row starts on 16 bytes
+    using bf16 = __nv_bfloat16;
     {
       TraceScope tr("ln_bwd", s);
-      const bool vec = a.m * esz % 16 == 0;   // every row starts on 16 bytes
-      if (sh.rows.threads <= 512) {
-        if (t == DT::BF16)
-          e = vec ? launch_bwd<__nv_bfloat16, 8, 512>(a, sh, a.parts, s)
-                  : launch_bwd<__nv_bfloat16, 1, 512>(a, sh, a.parts, s);
-        else
-          e = vec ? launch_bwd<float, 4, 512>(a, sh, a.parts, s)
-                  : launch_bwd<float, 1, 512>(a, sh, a.parts, s);
-      } else {
-        if (t == DT::BF16)
-          e = vec ? launch_bwd<__nv_bfloat16, 8, 1024>(a, sh, a.parts, s)
-                  : launch_bwd<__nv_bfloat16, 1, 1024>(a, sh, a.parts, s);
-        else
-          e = vec ? launch_bwd<float, 4, 1024>(a, sh, a.parts, s)
-                  : launch_bwd<float, 1, 1024>(a, sh, a.parts, s);
-      }
+      if (t == DT::BF16 && vec)
+        e = a.w_bf16 ? launch_bwd<bf16, bf16, 8>(a, sh, s) : launch_bwd<bf16, float, 8>(a, sh, s);
+      else if (t == DT::BF16)
+        e = a.w_bf16 ? launch_bwd<bf16, bf16, 1>(a, sh, s) : launch_bwd<bf16, float, 1>(a, sh, s);
+      else if (vec)
+        e = a.w_bf16 ? launch_bwd<float, bf16, 4>(a, sh, s) : launch_bwd<float, float, 4>(a, sh, s);
+      else
+        e = a.w_bf16 ? launch_bwd<float, bf16, 1>(a, sh, s) : launch_bwd<float, float, 1>(a, sh, s);
     }
     if (e != cudaSuccess || !cols) return e;
     TraceScope tr("ln_bwd_sum", s);
-    return launch_k(ln_cols_sum_kernel, sum_grid, block, 0, s, a);
+    return launch_k(ln_cols_sum_kernel, sum_grid, dim3(1024), 0, s, a);
   }
   // rows too wide for that: the column sums first, since dx may overwrite x or dy
   if (cols) {
@@ -676,7 +766,7 @@ cudaError_t bwd(Bwd a, DT t, void* ws, cudaStream_t s) {
       if (e != cudaSuccess) return e;
     }
     TraceScope tr("ln_bwd_sum", s);
-    e = launch_k(ln_cols_sum_kernel, sum_grid, block, 0, s, a);
+    e = launch_k(ln_cols_sum_kernel, sum_grid, dim3(1024), 0, s, a);
     if (e != cudaSuccess) return e;
   }
   if (a.dx) {
