@@ -246,134 +246,181 @@ __device__ __forceinline__ void ldw(const WT* p, int i, float none, float (&f)[V
   }
 }
 
-// Sums of a and b over the W warps of one row (row threadIdx.y of the block). Two calls in a row
-// take different buffers, so one barrier each is enough.
-template <int W>
-__device__ __forceinline__ float2 row_sum(float a, float b, float2 (*buf)[W]) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b += __shfl_xor_sync(0xffffffffu, b, o);
-  }
-  if constexpr (W == 1) return make_float2(a, b);
-  float2* mine = buf[threadIdx.y];
-  if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = make_float2(a, b);
-  __syncthreads();
-  float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int w = 0; w < W; ++w) {
-    s.x += mine[w].x;
-    s.y += mine[w].y;
-  }
-  return s;
-}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// Forward: W warps hold a row, E elements per lane, packed as they came; blockDim.y rows per block.
-// A row is read once and stays in registers over its two sums. What bounds it is instructions as
-// much as bytes: everything that a row costs apart from its elements (two reductions, addresses,
-// statistics) is paid per lane, so long rows go to few lanes. 16384 x 4096 bf16: 128 threads a
-// row with 32 elements each 67 us, two blocks of 512 threads over a ring with 8 elements each
-// 94 us (37 instructions an element), one warp with 128 elements 46 us.
-template <typename T, typename WT, int V, int E, int W>
+// Forward: W warps hold R rows, E elements of each per lane, packed as they came; blockDim.y such
+// sets per block. A row is read once and stays in registers over its two sums. What bounds it is
+// instructions as much as bytes, so what a row costs apart from its elements is kept small: W is
+// compiled in (constant offsets; with a run-time width 16384 x 4096 bf16 took 60 us instead
+// of 53), elements are worked on in pairs (fp32 x 2 instructions), and the R rows of a lane share
+// its weights: fp32 gamma and beta of one bf16 row are four times the row's own traffic to L1, which
+// bounded one row per warp (55 us, L1 78 % busy).
+template <typename T, typename WT, int V, int E, int W, int R>
 __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) ln_fwd_kernel(const Fwd a) {
-  constexpr int NV = E / V, ROWS = W > 4 ? 1 : 4 / W;
-  __shared__ float2 buf[2][ROWS][W];
+  constexpr int NV = E / V, Y = W > 4 ? 1 : 4 / W, STEP = 32 * W * V, P = V > 1 ? V / 2 : 1;
+  __shared__ float2 buf[2][Y][R][W];
   pdl_wait();
   pdl_trigger();
-  const int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.y;
-  const int m = r < a.T ? (int)a.m : 0;   // a row past the last one has no elements
-  const int c0 = threadIdx.x * V;         // vector i of a lane: column c0 + 32 W V i
-  const T* x = static_cast<const T*>(a.x) + r * a.m + c0;
-  Vec<T, V> v[NV];
-  float f[V];
+  const int64_t r0 = ((int64_t)blockIdx.x * Y + threadIdx.y) * R;
+  const int rows = (int)max((int64_t)0, min((int64_t)R, a.T - r0));   // of this set
+  const int c0 = threadIdx.x * V;         // vector i of a lane: column c0 + STEP i
+  const int m = (int)a.m;
+  const T* x = static_cast<const T*>(a.x) + r0 * a.m + c0;
+  Vec<T, V> v[R][NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (c0 + 32 * W * V * i < m) v[i].load(x + 32 * W * V * i);
-  float s = 0.f;
+  for (int j = 0; j < R; ++j)
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (c0 + 32 * W * V * i < m) {
-      v[i].get(f);
+    for (int i = 0; i < NV; ++i)
+      if (j < rows && c0 + STEP * i < m) v[j][i].load(x + j * (int64_t)m + STEP * i);
+  const float inv_m = 1.f / (float)m;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // a vector in pairs (a single element: the second of its pair is zero)
+  auto pairs = [](const Vec<T, V>& u, float2 (&f)[P]) {
+    float e[V];
+    u.get(e);
 #pragma unroll
-      for (int k = 0; k < V; ++k) s += f[k];
-    }
-  }
-  const float inv_m = 1.f / (float)a.m;
-  const float mean = row_sum<W>(s, 0.f, buf[0]).x * inv_m;
-  float s1 = 0.f, s2 = 0.f;
+    for (int k = 0; k < P; ++k) f[k] = make_float2(e[2 * k], V > 1 ? e[(2 * k + 1) % V] : 0.f);
+  };
+  // sums of p over the W warps, per row
+  auto reduce = [&](float2 (&p)[R], float2 (*b)[W]) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (c0 + 32 * W * V * i < m) {
-      v[i].get(f);
+    for (int j = 0; j < R; ++j)
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const float d = f[k] - mean;
-        s1 += d;
-        s2 += d * d;
+      for (int o = 16; o > 0; o >>= 1) {
+        p[j].x += __shfl_xor_sync(0xffffffffu, p[j].x, o);
+        p[j].y += __shfl_xor_sync(0xffffffffu, p[j].y, o);
+      }
+    if constexpr (W > 1) {
+      if (lane == 0)
+#pragma unroll
+        for (int j = 0; j < R; ++j) b[j][warp] = p[j];
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        p[j] = both(0.f);
+#pragma unroll
+        for (int w = 0; w < W; ++w) p[j] = __fadd2_rn(p[j], b[j][w]);
       }
     }
+  };
+  float mean[R];
+  float2 p[R], f[P];
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    float2 s = both(0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (j < rows && c0 + STEP * i < m) {
+        pairs(v[j][i], f);
+#pragma unroll
+        for (int k = 0; k < P; ++k) s = __fadd2_rn(s, f[k]);
+      }
+    }
+    p[j] = make_float2(s.x + s.y, 0.f);
   }
-  const float2 d = row_sum<W>(s1, s2, buf[1]);
-  const float dm = d.x * inv_m;
-  const float rstd = rstd_of(d.y * inv_m - dm * dm, a.eps);
-  T* y = static_cast<T*>(a.y) + r * a.m + c0;
+  reduce(p, buf[0][threadIdx.y]);
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    mean[j] = p[j].x * inv_m;
+    float2 s1 = both(0.f), s2 = both(0.f);
+    const float2 minus = make_float2(-mean[j], V > 1 ? -mean[j] : 0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (j < rows && c0 + STEP * i < m) {
+        pairs(v[j][i], f);
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          const float2 d = __fadd2_rn(f[k], minus);
+          s1 = __fadd2_rn(s1, d);
+          s2 = __ffma2_rn(d, d, s2);
+        }
+      }
+    }
+    p[j] = make_float2(s1.x + s1.y, s2.x + s2.y);
+  }
+  reduce(p, buf[1][threadIdx.y]);
+#pragma unroll
+  for (int j = 0; j < R; ++j) {   // p: dm and rstd
+    p[j].x *= inv_m;
+    p[j].y = rstd_of(p[j].y * inv_m - p[j].x * p[j].x, a.eps);
+    if (threadIdx.x == 0 && j < rows) {
+      if (a.mean) a.mean[r0 + j] = mean[j] + p[j].x;
+      if (a.rstd) a.rstd[r0 + j] = p[j].y;
+    }
+  }
+  T* y = static_cast<T*>(a.y) + r0 * a.m + c0;
   const WT* gamma = static_cast<const WT*>(a.gamma);
   const WT* beta = static_cast<const WT*>(a.beta);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = c0 + 32 * W * V * i;
+    const int c = c0 + STEP * i;
     if (c < m) {
       float g[V], b[V];
       ldw<WT, V>(gamma, c, 1.f, g);
       ldw<WT, V>(beta, c, 0.f, b);
-      v[i].get(f);
 #pragma unroll
-      for (int k = 0; k < V; ++k) g[k] = (f[k] - mean - dm) * rstd * g[k] + b[k];
-      stv<T, V>(y + 32 * W * V * i, g);
+      for (int j = 0; j < R; ++j) {
+        if (j < rows) {
+          // ((x - mean) - dm) rstd gamma + beta
+          float e[V];
+          pairs(v[j][i], f);
+#pragma unroll
+          for (int k = 0; k < P; ++k) {
+            const float2 g2 = make_float2(g[2 * k], g[(2 * k + 1) % V]);
+            const float2 b2 = make_float2(b[2 * k], b[(2 * k + 1) % V]);
+            const float2 d = __fadd2_rn(__fadd2_rn(f[k], both(-mean[j])), both(-p[j].x));
+            const float2 o = __ffma2_rn(__fmul2_rn(d, both(p[j].y)), g2, b2);
+            e[2 * k] = o.x;
+            if constexpr (V > 1) e[2 * k + 1] = o.y;
+          }
+          stv<T, V>(y + j * (int64_t)m + STEP * i, e);
+        }
+      }
     }
   }
-  if (threadIdx.x == 0 && m) {
-    if (a.mean) a.mean[r] = mean + dm;
-    if (a.rstd) a.rstd[r] = rstd;
-  }
 }
 
-constexpr int64_t kRegWidth = 16384;   // 16 warps x 32 lanes x 32 elements
+constexpr int64_t kRegWidth = 16384;
 
-template <typename T, typename WT, int V, int E, int W>
+template <typename T, typename WT, int V, int E, int W, int R>
 cudaError_t launch_fwd(const Fwd& a, cudaStream_t s) {
-  constexpr int ROWS = W > 4 ? 1 : 4 / W;
-  return launch_k(ln_fwd_kernel<T, WT, V, E, W>, dim3((unsigned)((a.T + ROWS - 1) / ROWS)),
-                  dim3(32 * W, ROWS), 0, s, a);
+  constexpr int Y = W > 4 ? 1 : 4 / W;
+  return launch_k(ln_fwd_kernel<T, WT, V, E, W, R>,
+                  dim3((unsigned)((a.T + Y * R - 1) / (Y * R))), dim3(32 * W, Y), 0, s, a);
 }
-// E elements per lane and as few warps as hold the row
-template <typename T, typename WT, int V, int E>
-cudaError_t fwd_warps(const Fwd& a, cudaStream_t s) {
-  if (a.m <= 32 * E) return launch_fwd<T, WT, V, E, 1>(a, s);
-  if (a.m <= 64 * E) return launch_fwd<T, WT, V, E, 2>(a, s);
-  if (a.m <= 128 * E) return launch_fwd<T, WT, V, E, 4>(a, s);
-  if constexpr (E < 128) {
-    if (a.m <= 256 * E) return launch_fwd<T, WT, V, E, 8>(a, s);
-    if constexpr (E < 64) return launch_fwd<T, WT, V, E, 16>(a, s);
-  }
-  return cudaErrorInvalidValue;
-}
-// E: 8 where a warp then holds the row; as much as 64 registers hold (128 bf16, 64 fp32 values)
-// where there are rows enough to fill the GPU that way; 32 otherwise (few rows: more lanes, less
-// latency) and for rows that do not start on 16 bytes (a register per value).
+// E x R values per lane. With rows enough to fill the GPU that way, as many as 64 registers hold
+// (128 of bf16, 64 of fp32, or 64 single elements, which take a register each): rows of 32
+// elements up to 4096 columns and longer pieces of fewer rows beyond, so that a block stays at 128
+// threads (fp32: 256); the barriers of 512 threads cost more than shared weights save (2048 x 16384
+// bf16: 45 us against 35 us). With few rows, one row and 32 elements, or 8 where a warp then
+// holds the row.
 template <typename T, typename WT, int V>
 cudaError_t fwd_width(const Fwd& a, cudaStream_t s) {
-  constexpr int kMost = V == 1 ? 32 : 256 / (int)sizeof(T);
-  if (a.m <= 256) return launch_fwd<T, WT, V, 8, 1>(a, s);
-  if constexpr (kMost > 32)
-    if (a.m > 1024 && a.T * ((a.m + 32 * kMost - 1) / (32 * kMost)) >= 8 * 148)
-      return fwd_warps<T, WT, V, kMost>(a, s);
-  return fwd_warps<T, WT, V, 32>(a, s);
+  constexpr int kHold = V == 1 ? 64 : 256 / (int)sizeof(T), kRows = kHold / 32;
+  const bool many = a.T * a.m >= (int64_t)kHold * 32 * 16 * 148;   // 16 warps on every SM
+  if (a.m <= 256)
+    return many ? launch_fwd<T, WT, V, 8, 1, kRows>(a, s) : launch_fwd<T, WT, V, 8, 1, 1>(a, s);
+  if (many) {
+    if (a.m <= 1024) return launch_fwd<T, WT, V, 32, 1, kRows>(a, s);
+    if (a.m <= 2048) return launch_fwd<T, WT, V, 32, 2, kRows>(a, s);
+    if (a.m <= 4096) return launch_fwd<T, WT, V, 32, 4, kRows>(a, s);
+    if constexpr (kHold == 128) {
+      if (a.m <= 8192) return launch_fwd<T, WT, V, 64, 4, 2>(a, s);
+      return launch_fwd<T, WT, V, 128, 4, 1>(a, s);
+    } else if constexpr (V > 1) {
+      if (a.m <= 8192) return launch_fwd<T, WT, V, 64, 4, 1>(a, s);
+      return launch_fwd<T, WT, V, 64, 8, 1>(a, s);
+    }
+  }
+  if (a.m <= 1024) return launch_fwd<T, WT, V, 32, 1, 1>(a, s);
+  if (a.m <= 2048) return launch_fwd<T, WT, V, 32, 2, 1>(a, s);
+  if (a.m <= 4096) return launch_fwd<T, WT, V, 32, 4, 1>(a, s);
+  if (a.m <= 8192) return launch_fwd<T, WT, V, 32, 8, 1>(a, s);
+  return launch_fwd<T, WT, V, 32, 16, 1>(a, s);
 }
 
 // ------------------------------------------------------------------ rows through a ring
-// A persistent block takes groups of blockDim.y consecutive rows (blockDim.x threads each). The
-// rows come through a ring of shared-memory slots by bulk copies, groups ahead, so that bytes are
+// A persistent block takes groups of consecutive rows. They come through a ring of shared-memory slots by bulk copies, groups ahead, so that bytes are
 // in flight whatever the block waits for. Elements are worked on in pairs (fp32 x 2
 // instructions): at bf16's two bytes an element, instructions count as much as bytes.
 // Rows that do not start on 16 bytes (V = 1) are copied as the 16-byte window around them.
@@ -430,8 +477,8 @@ struct Ring {
     }
   }
   __device__ __forceinline__ void init(uint8_t* buf, uint64_t* bars, int* abort_flag, int* err,
-                                       RingShape shape, int64_t T_, int64_t m) {
-    smem = buf; full = bars; sh = shape; rows = blockDim.y;
+                                       RingShape shape, int64_t T_, int64_t m, int rows_) {
+    smem = buf; full = bars; sh = shape; rows = rows_;
     ctl = umma::Ctl{abort_flag, err};
     row_bytes = m * sizeof(T);
     total = T_ * row_bytes;
@@ -451,7 +498,7 @@ struct Ring {
     for (int k = 0; k < sh.stages; ++k, next += gridDim.x)
       if (tid() == 0 && next < groups) fetch(next, k);
   }
-  // the current slot's row of this thread's group row, or false
+  // the current slot is filled (false: the wait ran out)
   __device__ __forceinline__ bool wait(int64_t g) {
     const bool ok = umma::wait_bounded(umma::smem_u32(full + s), ph, ctl, umma::kErrProducer,
                                        umma::kWaitLimitNs);
@@ -461,7 +508,7 @@ struct Ring {
       window(g, lo, hi, from, end);
       if (end < hi) {
         for (int64_t b = end + (int64_t)tid() * sizeof(T); b < hi;
-             b += (int64_t)blockDim.x * rows * sizeof(T))
+             b += (int64_t)blockDim.x * blockDim.y * sizeof(T))
 #pragma unroll
           for (int k = 0; k < ARR; ++k)
             *reinterpret_cast<T*>(smem + (size_t)(s * ARR + k) * sh.slot + (lo & 15) + (b - lo)) =
@@ -471,9 +518,10 @@ struct Ring {
     }
     return ok;
   }
-  __device__ __forceinline__ const T* row(int64_t g, int k) const {
+  // row `r` of the current slot's group
+  __device__ __forceinline__ const T* row(int64_t g, int k, int r) const {
     return reinterpret_cast<const T*>(smem + (size_t)(s * ARR + k) * sh.slot +
-                                      ((g * rows * row_bytes) & 15) + threadIdx.y * row_bytes);
+                                      ((g * rows * row_bytes) & 15) + r * row_bytes);
   }
   // After the barrier of the current group: the slot of the group before it has been read by every
   // thread and takes the next group to come; on to the next slot.
@@ -495,39 +543,50 @@ struct Ring {
   }
 };
 
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-
-// Backward. dx leaves from the block; a thread's columns (32 of them: vector i starts at column
-// (i blockDim.x + threadIdx.x) V) are the same in every row, so its shares of dgamma and dbeta stay
-// in 64 registers to the end, are added over the block's rows in shared memory and written once per
-// block. Per group there is one barrier: it completes the row sums, and it frees the slot of the
-// group before, which was read for the last time since the previous barrier.
-template <typename T, typename WT, int V>
-__global__ void __launch_bounds__(512, 1) ln_bwd_ring_kernel(const Bwd a, const RingShape shape) {
+// Backward. A thread has the same E columns in every row (vector i starts at column
+// (i blockDim.x + threadIdx.x) V), so its shares of dgamma and dbeta stay in registers to the end,
+// are added over the block's rows in shared memory and written once per block; E = 8 keeps its
+// gammas too. A group is R rows for each of blockDim.y sets of threads. Per group there is one barrier:
+// it completes the row sums, and it frees the slot of the group before, which was read for
+// the last time since the previous barrier; x and dy are read from their slot twice rather than
+// kept in registers.
+template <typename T, typename WT, int V, int E, int R>
+__global__ void __launch_bounds__(1024, 1) ln_bwd_ring_kernel(const Bwd a, const RingShape shape) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kMaxStages];
-  __shared__ float2 buf[2][16];
+  __shared__ float2 buf[2][32 * R];
   __shared__ int abort_flag;
-  constexpr int NV = 32 / V, P = V > 1 ? V / 2 : 1;
+  constexpr int NV = E / V, P = V > 1 ? V / 2 : 1;
+  constexpr bool KEEP = E == 8;
   const int m = (int)a.m, warps = blockDim.x >> 5, step = blockDim.x * V;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Ring<T, V, 2> ring;
   ring.src[0] = static_cast<const char*>(a.x);
   ring.src[1] = static_cast<const char*>(a.dy);
-  ring.init(smem, full, &abort_flag, a.err, shape, a.T, a.m);
+  ring.init(smem, full, &abort_flag, a.err, shape, a.T, a.m, blockDim.y * R);
   pdl_wait();
   pdl_trigger();
   ring.start();
   const WT* gamma = static_cast<const WT*>(a.gamma);
   const int c0 = threadIdx.x * V;
-  float ag[32], ab[32];
+  float gm[KEEP ? NV : 1][V];
+  if constexpr (KEEP) {
 #pragma unroll
-  for (int k = 0; k < 32; ++k) ag[k] = ab[k] = 0.f;
-  float mean_n = 0.f, rstd_n = 0.f;          // of the next group's row
+    for (int i = 0; i < NV; ++i)
+      if (c0 + i * step < m) ldw<WT, V>(gamma, c0 + i * step, 1.f, gm[i]);
+  }
+  float ag[E], ab[E];
+#pragma unroll
+  for (int k = 0; k < E; ++k) ag[k] = ab[k] = 0.f;
+  float mean_n[R], rstd_n[R];                // of the next group's rows
   auto stats = [&](int64_t g) {
-    const int64_t r = g * ring.rows + threadIdx.y;
-    if (r < a.T) {
-      mean_n = __ldg(a.mean + r);
-      rstd_n = __ldg(a.rstd + r);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const int64_t r = g * ring.rows + threadIdx.y * R + j;
+      if (r < a.T) {
+        mean_n[j] = __ldg(a.mean + r);
+        rstd_n[j] = __ldg(a.rstd + r);
+      }
     }
   };
   stats(blockIdx.x);
@@ -535,97 +594,118 @@ __global__ void __launch_bounds__(512, 1) ln_bwd_ring_kernel(const Bwd a, const 
   bool bad = false;
   int turn = 0;
   for (int64_t g = blockIdx.x; g < ring.groups; g += gridDim.x) {
-    const int64_t r = g * ring.rows + threadIdx.y;
-    const int live = r < a.T ? m : 0;
-    const float mean = mean_n, rstd = rstd_n;
+    const int64_t r0 = g * ring.rows + threadIdx.y * R;
+    const int rows = (int)max((int64_t)0, min((int64_t)R, a.T - r0));
+    float mean[R], rstd[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      mean[j] = mean_n[j];
+      rstd[j] = rstd_n[j];
+    }
     const bool ok = ring.wait(g);
-    const T* px = ring.row(g, 0) + c0;
-    const T* pd = ring.row(g, 1) + c0;
-    float2 s1 = both(0.f), s2 = both(0.f);
-    int c = c0;
+    const T* px = ring.row(g, 0, threadIdx.y * R) + c0;
+    const T* pd = ring.row(g, 1, threadIdx.y * R) + c0;
+    float2* sums = buf[turn] + threadIdx.y * R * warps;   // (the other one may still be read)
+    turn ^= 1;
 #pragma unroll
-    for (int i = 0; i < NV; ++i, c += step) {
-      if (c < live) {
-        Vec<T, V> vx, vd;
-        float x[V], d[V], w[V];
-        vx.load(px + i * step);
-        vd.load(pd + i * step);
-        vx.get(x);
-        vd.get(d);
-        ldw<WT, V>(gamma, c, 1.f, w);
-        if constexpr (V == 1) {
-          const float h = (x[0] - mean) * rstd, gk = d[0] * w[0];
-          ag[i] += d[0] * h;
-          ab[i] += d[0];
-          s1.x += gk;
-          s2.x += gk * h;
-        } else {
+    for (int j = 0; j < R; ++j) {
+      float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
-          for (int k = 0; k < P; ++k) {
-            const float2 d2 = make_float2(d[2 * k], d[2 * k + 1]);
-            const float2 h = __fmul2_rn(
-                __fadd2_rn(make_float2(x[2 * k], x[2 * k + 1]), both(-mean)), both(rstd));
-            const float2 gk = __fmul2_rn(d2, make_float2(w[2 * k], w[2 * k + 1]));
-            float2* eg = reinterpret_cast<float2*>(ag + i * V) + k;
-            float2* eb = reinterpret_cast<float2*>(ab + i * V) + k;
-            *eg = __ffma2_rn(d2, h, *eg);
-            *eb = __fadd2_rn(*eb, d2);
-            s1 = __fadd2_rn(s1, gk);
-            s2 = __ffma2_rn(gk, h, s2);
+      for (int i = 0; i < NV; ++i) {
+        const int c = c0 + i * step;
+        if (j < rows && c < m) {
+          Vec<T, V> vx, vd;
+          float x[V], d[V], w[V];
+          vx.load(px + j * m + i * step);
+          vd.load(pd + j * m + i * step);
+          vx.get(x);
+          vd.get(d);
+          if constexpr (KEEP) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) w[k] = gm[i][k];
+          } else {
+            ldw<WT, V>(gamma, c, 1.f, w);
+          }
+          if constexpr (V == 1) {
+            const float h = (x[0] - mean[j]) * rstd[j], gk = d[0] * w[0];
+            ag[i] += d[0] * h;
+            ab[i] += d[0];
+            s1.x += gk;
+            s2.x += gk * h;
+          } else {
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+              const float2 d2 = make_float2(d[2 * k], d[2 * k + 1]);
+              const float2 h = __fmul2_rn(
+                  __fadd2_rn(make_float2(x[2 * k], x[2 * k + 1]), both(-mean[j])), both(rstd[j]));
+              const float2 gk = __fmul2_rn(d2, make_float2(w[2 * k], w[2 * k + 1]));
+              float2* eg = reinterpret_cast<float2*>(ag + i * V) + k;
+              float2* eb = reinterpret_cast<float2*>(ab + i * V) + k;
+              *eg = __ffma2_rn(d2, h, *eg);
+              *eb = __fadd2_rn(*eb, d2);
+              s1 = __fadd2_rn(s1, gk);
+              s2 = __ffma2_rn(gk, h, s2);
+            }
           }
         }
       }
-    }
-    float2 t = make_float2(s1.x + s1.y, s2.x + s2.y);
+      // both sums at once: the lower half-warp goes on with s1, the upper one with s2
+      const float t1 = s1.x + s1.y, t2 = s2.x + s2.y;
+      float t = (lane & 16) ? t2 : t1;
+      t += __shfl_xor_sync(0xffffffffu, (lane & 16) ? t1 : t2, 16);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
-      t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
+      for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      if ((lane & 15) == 0) reinterpret_cast<float*>(sums + j * warps + warp)[lane >> 4] = t;
     }
-    float2* sums = buf[turn] + threadIdx.y * warps;   // (the other one may still be read)
-    turn ^= 1;
-    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = t;
     if (g + gridDim.x < ring.groups) stats(g + gridDim.x);
     bad = __syncthreads_or(!ok);
     if (bad) break;
     ring.release();
     if (a.dx) {
-      if (warps > 1) {
-        t = both(0.f);
-        for (int w = 0; w < warps; ++w) {
-          t.x += sums[w].x;
-          t.y += sums[w].y;
+      T* dx = static_cast<T*>(a.dx) + r0 * a.m + c0;
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        // the row's sums over its warps, by the warp's lanes
+        float2 t = lane < warps ? sums[j * warps + lane] : both(0.f);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
+          t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
         }
-      }
-      const float c1 = t.x * inv_m, c2 = t.y * inv_m;
-      T* dx = static_cast<T*>(a.dx) + r * a.m + c0;
-      c = c0;
+        const float c1 = t.x * inv_m, c2 = t.y * inv_m;
 #pragma unroll
-      for (int i = 0; i < NV; ++i, c += step) {
-        if (c < live) {
-          Vec<T, V> vx, vd;
-          float x[V], d[V], w[V];
-          vx.load(px + i * step);
-          vd.load(pd + i * step);
-          vx.get(x);
-          vd.get(d);
-          ldw<WT, V>(gamma, c, 1.f, w);
-          // rstd (g - c1 - xh c2)
-          if constexpr (V == 1) {
-            d[0] = rstd * (d[0] * w[0] - c1 - (x[0] - mean) * rstd * c2);
-          } else {
+        for (int i = 0; i < NV; ++i) {
+          const int c = c0 + i * step;
+          if (j < rows && c < m) {
+            Vec<T, V> vx, vd;
+            float x[V], d[V], w[V];
+            vx.load(px + j * m + i * step);
+            vd.load(pd + j * m + i * step);
+            vx.get(x);
+            vd.get(d);
+            if constexpr (KEEP) {
 #pragma unroll
-            for (int k = 0; k < P; ++k) {
-              const float2 h = __fmul2_rn(
-                  __fadd2_rn(make_float2(x[2 * k], x[2 * k + 1]), both(-mean)), both(rstd));
-              float2 e = __ffma2_rn(make_float2(d[2 * k], d[2 * k + 1]),
-                                    make_float2(w[2 * k], w[2 * k + 1]), both(-c1));
-              e = __fmul2_rn(__ffma2_rn(h, both(-c2), e), both(rstd));
-              d[2 * k] = e.x;
-              d[2 * k + 1] = e.y;
+              for (int k = 0; k < V; ++k) w[k] = gm[i][k];
+            } else {
+              ldw<WT, V>(gamma, c, 1.f, w);
             }
+            // rstd (g - c1 - xh c2)
+            if constexpr (V == 1) {
+              d[0] = rstd[j] * (d[0] * w[0] - c1 - (x[0] - mean[j]) * rstd[j] * c2);
+            } else {
+#pragma unroll
+              for (int k = 0; k < P; ++k) {
+                const float2 h = __fmul2_rn(
+                    __fadd2_rn(make_float2(x[2 * k], x[2 * k + 1]), both(-mean[j])), both(rstd[j]));
+                float2 e = __ffma2_rn(make_float2(d[2 * k], d[2 * k + 1]),
+                                      make_float2(w[2 * k], w[2 * k + 1]), both(-c1));
+                e = __fmul2_rn(__ffma2_rn(h, both(-c2), e), both(rstd[j]));
+                d[2 * k] = e.x;
+                d[2 * k + 1] = e.y;
+              }
+            }
+            stv<T, V>(dx + j * (int64_t)m + i * step, d);
           }
-          stv<T, V>(dx + i * step, d);
         }
       }
     }
@@ -635,10 +715,10 @@ __global__ void __launch_bounds__(512, 1) ln_bwd_ring_kernel(const Bwd a, const 
     return;
   }
   if (!a.part) return;
-  // the block's column sums, its rows added in order; no copy is in flight any more
+  // the block's column sums, its sets of threads added in order; no copy is in flight any more
   float* out_g = a.part + (int64_t)blockIdx.x * m;
   float* out_b = a.part + ((int64_t)gridDim.x + blockIdx.x) * m;
-  float* sh = reinterpret_cast<float*>(smem);    // [rows][2][m]
+  float* sh = reinterpret_cast<float*>(smem);    // [sets][2][m]
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -654,7 +734,7 @@ __global__ void __launch_bounds__(512, 1) ln_bwd_ring_kernel(const Bwd a, const 
   __syncthreads();
   for (int c = ring.tid(); c < m; c += blockDim.x * blockDim.y) {
     float g = 0.f, b = 0.f;
-    for (int y = 0; y < ring.rows; ++y) {
+    for (int y = 0; y < (int)blockDim.y; ++y) {
       g += sh[(y * 2) * m + c];
       b += sh[(y * 2 + 1) * m + c];
     }
@@ -665,37 +745,49 @@ __global__ void __launch_bounds__(512, 1) ln_bwd_ring_kernel(const Bwd a, const 
 
 constexpr int kMaxParts = 148;   // one block per SM
 
-// Threads per row, rows per group and ring for a width; stages < 2: a row is too wide for the ring.
-// A group is at most 64 KB of x and dy (three slots in flight), and no larger than leaves a group
-// for every SM.
+// Shape of the one-pass backward for a width; stages < 2: a row is too wide for the ring. E = 8 up to
+// 8192 columns (a row then has at most 1024 threads), 16 beyond; `sets` sets of threads and R rows
+// each (two share their addresses and the barrier; one where single elements use up the registers)
+// make a group, at most 64 KB of x and dy (three slots in flight) and no more than leaves
+// a group for every SM.
 struct GroupShape {
-  int threads, rows;
+  int threads, sets, E, R;
   RingShape ring;
   size_t smem;
 };
-GroupShape group_shape(int64_t T, int64_t m, int esz) {
+GroupShape group_shape(int64_t T, int64_t m, int esz, bool vec) {
   GroupShape sh;
-  sh.threads = 32 * (int)((m + 1023) / 1024);   // 32 elements per thread
-  int64_t rows = std::min<int64_t>(512 / sh.threads, 64 * 1024 / (2 * m * esz));
-  rows = std::min<int64_t>(rows, (T + kMaxParts - 1) / kMaxParts);
-  sh.rows = (int)std::max<int64_t>(1, rows);
+  sh.E = m <= 8192 ? 8 : 16;
+  sh.threads = 32 * (int)((m + 32 * sh.E - 1) / (32 * sh.E));
+  const int64_t fit = 64 * 1024 / (2 * m * esz);                  // rows in 64 KB
+  const int64_t share = (T + kMaxParts - 1) / kMaxParts;          // rows per SM
+  const int64_t rows = std::max<int64_t>(1, std::min(fit, share));
+  sh.R = sh.E == 8 && vec && rows >= 2 ? 2 : 1;
+  sh.sets = (int)std::max<int64_t>(1, std::min<int64_t>(1024 / sh.threads, rows / sh.R));
   // the window around unaligned rows needs up to 30 bytes more
-  sh.ring.slot = (int)(((int64_t)sh.rows * m * esz + 31) / 16 * 16);
+  sh.ring.slot = (int)(((int64_t)sh.sets * sh.R * m * esz + 31) / 16 * 16);
   const int64_t stage = 2 * (int64_t)sh.ring.slot;
   sh.ring.stages = (int)std::min<int64_t>(kMaxStages, kRingBytes / stage);
   // at the end the ring's memory holds the block's column sums
-  sh.smem = std::max((size_t)(sh.ring.stages * stage), (size_t)sh.rows * 2 * m * sizeof(float));
+  sh.smem = std::max((size_t)(sh.ring.stages * stage), (size_t)sh.sets * 2 * m * sizeof(float));
   return sh;
 }
 
-template <typename T, typename WT, int V>
-cudaError_t launch_bwd(const Bwd& a, const GroupShape& sh, cudaStream_t s) {
-  auto kern = ln_bwd_ring_kernel<T, WT, V>;
+template <typename T, typename WT, int V, int E, int R>
+cudaError_t launch_bwd_er(const Bwd& a, const GroupShape& sh, cudaStream_t s) {
+  auto kern = ln_bwd_ring_kernel<T, WT, V, E, R>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem);
   if (e != cudaSuccess) return e;
-  return launch_k(kern, dim3((unsigned)a.parts), dim3((unsigned)sh.threads, (unsigned)sh.rows),
+  return launch_k(kern, dim3((unsigned)a.parts), dim3((unsigned)sh.threads, (unsigned)sh.sets),
                   sh.smem, s, a, sh.ring);
+}
+template <typename T, typename WT, int V>
+cudaError_t launch_bwd(const Bwd& a, const GroupShape& sh, cudaStream_t s) {
+  if (sh.E == 16) return launch_bwd_er<T, WT, V, 16, 1>(a, sh, s);
+  if constexpr (V > 1)
+    if (sh.R == 2) return launch_bwd_er<T, WT, V, 8, 2>(a, sh, s);
+  return launch_bwd_er<T, WT, V, 8, 1>(a, sh, s);
 }
 
 int row_blocks(int64_t T) { return (int)std::min<int64_t>(T, 148 * 8); }
@@ -734,11 +826,11 @@ cudaError_t bwd(Bwd a, DT t, void* ws, cudaStream_t s) {
   a.err = device_error_word();
   if (!a.err) return cudaErrorUnknown;
   cudaError_t e = cudaSuccess;
-  const GroupShape sh = a.m <= kRegWidth ? group_shape(a.T, a.m, esz) : GroupShape{};
+  const bool vec = a.m * esz % 16 == 0;   // every row starts on 16 bytes
+  const GroupShape sh = a.m <= kRegWidth ? group_shape(a.T, a.m, esz, vec) : GroupShape{};
   if (a.m <= kRegWidth && sh.ring.stages >= 2) {
-    const int64_t groups = (a.T + sh.rows - 1) / sh.rows;
+    const int64_t groups = (a.T + sh.sets * sh.R - 1) / (sh.sets * sh.R);
     a.parts = (int)std::min<int64_t>(groups, kMaxParts);
-    const bool vec = a.m * esz % 16 == 0;   // every row starts on 16 bytes
     using bf16 = __nv_bfloat16;
     {
       TraceScope tr("ln_bwd", s);
