@@ -954,14 +954,14 @@ poetx_status check_orth(const char* what, orth::Problem* p, int64_t batch, int64
   constexpr int64_t kMaxSide = 65536, kMaxBatch = 65535;
   if (batch < 0 || m < 0 || n < 0)
     return fail(POETX_ERR_INVALID_ARG, "%s: negative size", what);
-  if (batch > kMaxBatch || m > kMaxSide || n > kMaxSide ||
-      batch * ((m + 127) / 128) * ((n + 127) / 128) > (int64_t)INT32_MAX)
-    return fail(POETX_ERR_SHAPE, "%s: %lld matrices of %lld x %lld exceed the supported sizes", what,
-                (long long)batch, (long long)m, (long long)n);
   if (!coeffs) return fail(POETX_ERR_INVALID_ARG, "%s: coeffs is NULL", what);
   if (steps < 1 || steps > POETX_ORTH_MAX_STEPS)
     return fail(POETX_ERR_INVALID_ARG, "%s: steps=%d is not in 1..%d", what, (int)steps,
                 POETX_ORTH_MAX_STEPS);
+  if (batch > kMaxBatch || m > kMaxSide || n > kMaxSide ||
+      batch * ((m + 127) / 128) * ((n + 127) / 128) * 3 * steps > (int64_t)INT32_MAX / 16)
+    return fail(POETX_ERR_SHAPE, "%s: %lld matrices of %lld x %lld exceed the supported sizes", what,
+                (long long)batch, (long long)m, (long long)n);
   if (!(eps >= 0.f) || !std::isfinite(eps) || !std::isfinite(scale))
     return fail(POETX_ERR_INVALID_ARG, "%s: eps must be finite and >= 0, scale finite", what);
   if (!orth::make_plan(coeffs, steps, plan))

@@ -5,12 +5,20 @@
 //
 // with X laid out so that it has no more rows r than columns k (a taller input is transposed on
 // its way in and back on its way out: X (X^T X) = (X X^T) X). Per step three products:
-//   gram    A = X X^T, its epilogue also writes H = b I + c A          (symmetric)
-//   square  B = a I + A H = a I + b A + c A^2                          (symmetric)
-//   update  X <- B X                                                   (skew for skew X)
-// The polynomial's lower terms ride on the diagonals of H and B, so no epilogue reads a matrix
-// back. Symmetric (and skew) results are computed on the tiles on and above the diagonal; the
-// epilogue stores every other tile twice, the second time transposed (and negated).
+//   gram    A = X X^T                                  (symmetric)
+//   square  B = a I + b A + c A A                      (symmetric; the epilogue reads A's tile)
+//   update  X <- B X                                   (skew for skew X)
+// a X rides on B's diagonal. Symmetric (and skew) results may be computed on the tiles on and above
+// the diagonal only; the epilogue then stores every other tile twice, the second time
+// transposed (and negated).
+//
+// All steps of all matrices run in one launch. Its tiles, in the order step, product, matrix,
+// tile, are handed out one by one from a counter to the clusters that run; a tile's operands are
+// loaded once the product before it is complete for its matrix (a count per matrix, raised by
+// the epilogue warps after their stores). Every tile that a cluster waits for was handed out
+// earlier, to a cluster that runs, so the waits end whatever else shares the GPU. Fifteen launches
+// would pay for a ramp, a partial wave of tiles and a drain each: at 36 blocks of 512 two thirds
+// of their time.
 //
 // Precision. Operands are fp16 parts of scaled values with fp32 accumulation: x = hi + lo,
 // hi = fp16(x), lo = fp16(x - hi), which carries 22 bits. The scales are powers of two chosen on
@@ -27,10 +35,7 @@
 //     rms: 1.4e-3 for an update of a few strong directions over a background (single-part X
 //     2.0e-3, and 9.5e-3 with a background of 3 % of the strongest); bf16 rounding alone is
 //     1.7e-3.
-#include "orth.h"
-#include "umma_ptx.cuh"
-
-#include <cuda_fp16.h>
+#include "orth_mma.cuh"
 
 #include <algorithm>
 #include <cmath>
@@ -39,10 +44,7 @@ namespace poetx {
 namespace orth {
 namespace {
 
-using namespace umma;
-
 constexpr int BK = 64;
-constexpr int kStages = 5;
 constexpr int kEpiWarps = 8;               // two per TMEM lane quarter, half of the columns each
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 // Registers per thread at launch, then of warps 0..3 (which only issue copies and MMAs) and of the
@@ -51,50 +53,94 @@ constexpr int kRegsLaunch = 168, kRegsIssue = 56, kRegsEpi = 224;
 static_assert(128 * kRegsIssue + 32 * kEpiWarps * kRegsEpi <= kThreads * kRegsLaunch,
               "the register split must fit the launch's registers");
 constexpr int kChunk = 2;                  // K blocks per accumulator of an fp32 result
-constexpr int kPartBytes = 128 * BK * 2;   // one operand of one CTA and stage: 128 rows x 64
-constexpr int kEpiStage = 8192;            // per epilogue warp
-constexpr size_t kSmem = (size_t)kStages * 2 * kPartBytes + kEpiWarps * kEpiStage + 1024 + 256;
+constexpr int kPiece = 4096;               // 32 rows x 64 columns of fp16
+constexpr int kEpiStage = 2 * kPiece;      // per epilogue warp
+// Tile numbers handed from the producer to the others. The producer is at most two tiles (the
+// accumulators) and a ring of one-block tiles ahead of the epilogue, so that no slot's barriers
+// pass two phases while a role still waits for the first.
+constexpr int kSlots = 8;
 
-// ------------------------------------------------------------------ products
-enum : int { kToMaps = 0, kRows = 1, kTransposed = 2, kPacked = 3 };
-
-struct Prod {
-  int tiles_m, tiles_n, per, total, sym, batch;
-  int rows, cols;            // padded extents of the output (kToMaps)
-  int nk, nseg;              // K blocks per segment; segment s multiplies parts pa[s], pb[s]
-  int head, chunk;           // K blocks of a tile's first accumulator and of the later ones
-  int pa[3], pb[3];
-  float f0, d0, f1, d1;      // output o: acc * f + (i == j) * d
-  int has1, lo;              // a second output; both outputs in two parts
-  float mirror;              // sym: sign of the mirrored tile
-  int fmode;                 // where the result goes
-  void* out;                 // the caller's array (fmode != kToMaps)
-  int out_f32, vec;          // its type; rows start on 16 bytes
-  long long um, un;          // valid rows and columns of the result
-  int* err;
+// ------------------------------------------------------------------ the work
+// Tile shapes. CG = 1: 128 x 128 tiles of one CTA; CG = 2: 256 x TN tiles of a CTA pair
+// (cta_group::2: each CTA holds 128 rows of A, half of B's columns and 128 rows of the result).
+template <int CG_, int TN_>
+struct Shape {
+  static constexpr int CG = CG_, TM = 128 * CG_, TN = TN_;
+  static constexpr int BN = TN / CG;                    // columns of B that a CTA loads
+  static constexpr int A_BYTES = 128 * BK * 2, B_BYTES = BN * BK * 2;
+  // (three 32 KB stages are enough while X fits L2, and cost 15 % where it does not)
+  static constexpr int STAGES = A_BYTES + B_BYTES > 24576 ? 5 : 6;
+  static constexpr int COLS = TN / 2;                   // result columns of an epilogue warp
+  static constexpr size_t SMEM =
+      (size_t)STAGES * (A_BYTES + B_BYTES) + kEpiWarps * kEpiStage + 1024 + 512;
 };
 
-struct Tile {
-  int g, mb, nb;
+
+struct Kind {
+  int tiles_m, tiles_n, per;   // tile grid of a matrix; tiles computed
+  int sym, cols, nk;           // sym: on and above the diagonal; padded columns; K blocks a segment
 };
-// Symmetric results: row by row over the tiles on and above the diagonal. Others: bands of 16
-// row tiles sweep the columns, so a band of the left operand stays in L2 while X streams.
-__device__ __forceinline__ Tile decode(const Prod& p, int tile) {
-  Tile t;
-  t.g = tile / p.per;
-  int l = tile - t.g * p.per;
-  if (p.sym) {
+struct Job {
+  Kind k[3];
+  int batch, steps, per_step, total;   // tiles per step (all matrices) and in all
+  int R;                               // padded rows of every result
+  int exact, skew;
+  int fmode, out_f32, vec;             // the caller's array: layout, type, rows start on 16 bytes
+  void* out;
+  long long um, un;                    // its rows and columns (of the result as computed)
+  int *counter, *done, *err;           // tiles handed out; per matrix: epilogue warps finished
+  float f[3][kMaxSteps];               // result = acc f
+  float fa[kMaxSteps], da[kMaxSteps];  // square: + fa A + da I
+};
+struct Maps {
+  CUtensorMap xa[2], xb[2], xn[2];   // X: left operand, right operand K- and N-major,
+  CUtensorMap xs[2], xm[2];          //    pieces as computed and mirrored
+  CUtensorMap aa, ab, as, am;        // A: left and right operand, pieces
+  CUtensorMap ba, bs, bm;            // B: left operand, pieces
+};
+
+struct Work {
+  int t, kind, g, mb, nb;
+  bool last;
+};
+// Tile numbers count through step, product, matrix, tile. Symmetric results: row by row over the
+// tiles on and above the diagonal. Others: bands of 16 row tiles sweep the columns, so a band
+// of the left operand stays in L2 while X streams.
+template <typename S>
+__device__ __forceinline__ Work decode(const Job& j, int tile) {
+  Work w;
+  w.t = tile / j.per_step;
+  w.last = w.t + 1 == j.steps;
+  int l = tile - w.t * j.per_step;
+  w.kind = kGram;
+  while (w.kind < kUpdate && l >= j.batch * j.k[w.kind].per) l -= j.batch * j.k[w.kind++].per;
+  const Kind& k = j.k[w.kind];
+  w.g = l / k.per;
+  l -= w.g * k.per;
+  if (k.sym) {
+    constexpr int Q = S::TM / S::TN;
     int i = 0;
-    while (l >= p.tiles_n - i) l -= p.tiles_n - i++;
-    t.mb = i;
-    t.nb = i + l;
+    while (l >= k.tiles_n - Q * i) l -= k.tiles_n - Q * i++;
+    w.mb = i;
+    w.nb = Q * i + l;
   } else {
-    const int band = l / (16 * p.tiles_n), first = band * 16;
-    const int gm = min(16, p.tiles_m - first), w = l - band * 16 * p.tiles_n;
-    t.mb = first + w % gm;
-    t.nb = w / gm;
+    const int band = l / (16 * k.tiles_n), first = band * 16;
+    const int gm = min(16, k.tiles_m - first), r = l - band * 16 * k.tiles_n;
+    w.mb = first + r % gm;
+    w.nb = r / gm;
   }
-  return t;
+  return w;
+}
+// Part products of a tile: hi hi | hi lo, hi hi | lo hi, hi lo, hi hi, the small ones first.
+__device__ __forceinline__ int segments(const Job& j, const Work& w) {
+  return j.exact ? 3 : w.kind == kUpdate && !w.last ? 2 : 1;
+}
+__device__ __forceinline__ int part_a(int n, int seg) { return n == 3 && seg == 0; }
+__device__ __forceinline__ int part_b(int n, int seg) { return n > 1 && seg == n - 2; }
+// K blocks that the first accumulator of a tile sums: the small products and the first kChunk of the
+// large one for fp32 results, everything otherwise
+__device__ __forceinline__ int head_blocks(const Job& j, int n, int nk) {
+  return j.exact ? (n - 1) * nk + min(kChunk, nk) : n * nk;
 }
 
 template <int CG>
@@ -122,27 +168,24 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, 
       : "memory");
 }
 
-// kind::f16, fp16 operands, fp32 accumulator, 128 CG x 128 CG tile
-template <int CG, bool B_MN>
+// kind::f16, fp16 operands, fp32 accumulator, TM x TN tile; bit 16: B is N-major
+template <typename S>
 __device__ __forceinline__ constexpr uint32_t idesc() {
-  return (1u << 4) | ((B_MN ? 1u : 0u) << 16) | ((uint32_t)(128 * CG >> 3) << 17) |
-         ((uint32_t)(128 * CG >> 4) << 24);
+  return (1u << 4) | ((uint32_t)(S::TN >> 3) << 17) | ((uint32_t)(S::TM >> 4) << 24);
 }
 
-// wait_bounded (umma_ptx.cuh) without the call: a call would put the accumulated registers on the
-// stack, and setmaxnreg allows none.
-__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, Ctl c, int code,
-                                            uint64_t limit_ns = kWaitLimitNs,
-                                            bool stop_on_abort = true) {
-  if (mbar_try_wait(bar, parity)) return true;
+// until *cnt >= target
+__device__ __forceinline__ bool wait_done(const int* cnt, int target, Ctl c) {
+  if (ld_acquire_gpu(cnt) >= target) return true;
   const uint64_t t0 = global_ns();
   for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 31) == 0) {
-      if (stop_on_abort && *c.abort) return false;
-      if (global_ns() - t0 > limit_ns) {
+    __nanosleep(64);
+    if (ld_acquire_gpu(cnt) >= target) return true;
+    if ((it & 15) == 0) {
+      if (*c.abort) return false;
+      if (global_ns() - t0 > kLimitNs) {
         *c.abort = 1;
-        if (code) atomicCAS(c.err, 0, code);
+        atomicCAS(c.err, 0, (int)kErrDependency);
         return false;
       }
     }
@@ -162,88 +205,80 @@ __device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&r)[4])
                : "memory");
 }
 
-// One 32-row x 64-column piece of a warp to the fp16 maps: both outputs, both parts, and the
-// mirrored piece of an off-diagonal tile. The warp's 8 KB stage is two halves that alternate, so
-// a piece is packed while the previous one's copy still reads its half. A piece lies in its
-// half in the 128-byte swizzle (16-byte unit u of row i at u ^ (i & 7)); the mirrored piece is
-// read from there by transposing 8 x 8 blocks and lies in the 64-byte swizzle (unit u of row j at
-// u ^ (j / 2 & 3)): neither side has bank conflicts.
-__device__ __forceinline__ void emit_maps(const Prod& p, const CUtensorMap* out0,
-                                          const CUtensorMap* out1, const CUtensorMap* mir0,
-                                          const CUtensorMap* mir1, const float* v, int g, int row0,
-                                          int col0, bool mirror, uint32_t stage, int lane,
-                                          int& chunk) {
+// One 32-row x 64-column piece of a warp to the fp16 maps, in one or two parts, and the mirrored
+// piece of an off-diagonal tile. The value of element (i, j) is v f + (i == j) d. The parts are
+// packed into the halves of the warp's stage in the 128-byte swizzle (16-byte unit u of row i at
+// u ^ (i & 7)) and copied out together. For the mirror each half is then transposed in place, in 8 x 8
+// blocks through registers, into the 64-byte swizzle (unit u of row j at u ^ (j / 2 & 3)): no bank
+// conflicts either way. (Plain 16-byte stores instead of the copies: the same time where many tiles
+// hide it, 15 to 30 % more where a product waits for the one before, which then waits for the
+// stores' fence.)
+__device__ __forceinline__ void emit_maps(const CUtensorMap* out, const CUtensorMap* mir,
+                                          const float* v, float f, float d, int parts, int batch,
+                                          int g, int row0, int col0, bool mirror, uint32_t flip,
+                                          uint32_t stage, int lane) {
+  if (lane == 0) bulk_wait_read<0>();   // the copies of the piece before have read the stage
+  __syncwarp();
 #pragma unroll 1
-  for (int o = 0; o <= p.has1; ++o) {
-    const float f = o ? p.f1 : p.f0, d = o ? p.d1 : p.d0;
-#pragma unroll 1
-    for (int part = 0; part <= p.lo; ++part) {
-      int dq = row0 + lane - col0;            // the diagonal's column of this row's 64
-      asm volatile("" : "+r"(dq));            // (not 64 comparisons kept over the loops)
-      const int z = part * p.batch + g;
-      const uint32_t half = stage + (chunk & 1) * 4096;
-      if (lane == 0) bulk_wait_read<1>();
-      __syncwarp();
+  for (int part = 0; part < parts; ++part) {
+    int dq = row0 + lane - col0;        // the diagonal's column of this row's 64
+    asm volatile("" : "+r"(dq));        // (not 64 comparisons kept over the parts)
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        uint32_t h[4];
+    for (int u = 0; u < 8; ++u) {
+      uint32_t h[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int c = 8 * u + 2 * q;
-          const float a = v[c] * f + (dq == c ? d : 0.f);
-          const float b = v[c + 1] * f + (dq == c + 1 ? d : 0.f);
-          __half2 w = __floats2half2_rn(a, b);
-          if (part) w = __floats2half2_rn(a - __low2float(w), b - __high2float(w));
-          h[q] = *reinterpret_cast<uint32_t*>(&w);
-        }
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                         half + lane * 128 + ((u ^ (lane & 7)) << 4)),
-                     "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
-                     : "memory");
+      for (int q = 0; q < 4; ++q) {
+        const int c = 8 * u + 2 * q;
+        const float a = v[c] * f + (dq == c ? d : 0.f);
+        const float b = v[c + 1] * f + (dq == c + 1 ? d : 0.f);
+        __half2 w = __floats2half2_rn(a, b);
+        if (part) w = __floats2half2_rn(a - __low2float(w), b - __high2float(w));
+        h[q] = *reinterpret_cast<const uint32_t*>(&w);
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) {
-        store_box(o ? out1 : out0, half, col0, row0, z);
-        bulk_commit();
-      }
-      ++chunk;
-      if (mirror) {
-        const uint32_t other = stage + (chunk & 1) * 4096;
-        if (lane == 0) bulk_wait_read<1>();
-        __syncwarp();
-        const uint32_t flip = p.mirror < 0.f ? 0x80008000u : 0u;
-        // lane l names row l of the piece's 32 for the load, and for the store row l % 8 of the
-        // unit's eight in 16-byte unit l / 8
-        const uint32_t src = half + lane * 128;
-        const int blk = lane >> 3, jj = lane & 7;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          uint32_t r[4];
-          ldmatrix4_trans(src + ((u ^ (lane & 7)) << 4), r);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) r[q] ^= flip;
-          stmatrix4(other + (8 * u + jj) * 64 + ((blk ^ ((jj >> 1) & 3)) << 4), r);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          store_box(o ? mir1 : mir0, other, row0, col0, z);
-          bulk_commit();
-        }
-        ++chunk;
-      }
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                       stage + part * kPiece + lane * 128 + ((u ^ (lane & 7)) << 4)),
+                   "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                   : "memory");
     }
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if (lane == 0) {
+    for (int part = 0; part < parts; ++part)
+      store_box(out, stage + part * kPiece, col0, row0, part * batch + g);
+    bulk_commit();
+  }
+  if (!mirror) return;
+  // lane l names row l of the piece's 32 for the load, and for the store row l % 8 of the unit's
+  // eight in 16-byte unit l / 8
+  const int blk = lane >> 3, jj = lane & 7;
+#pragma unroll 1
+  for (int part = 0; part < parts; ++part) {
+    const uint32_t half = stage + part * kPiece;
+    uint32_t r[8][4];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      ldmatrix4_trans(half + lane * 128 + ((u ^ (lane & 7)) << 4), r[u]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) r[u][q] ^= flip;
+    }
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      stmatrix4(half + (8 * u + jj) * 64 + ((blk ^ ((jj >> 1) & 3)) << 4), r[u]);
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if (lane == 0) {
+    for (int part = 0; part < parts; ++part)
+      store_box(mir, stage + part * kPiece, row0, col0, part * batch + g);
+    bulk_commit();
   }
 }
 
-__device__ __forceinline__ void put(void* out, long long at, float x, int f32) {
-  if (f32) static_cast<float*>(out)[at] = x;
-  else static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(x);
-}
-
 // The same piece to the caller's array.
-__device__ __forceinline__ void emit_user(const Prod& p, const float* v, int g, int row0,
+__device__ __forceinline__ void emit_user(const Job& p, const float* v, float f, int g, int row0,
                                           int col0, uint8_t* stage, int lane) {
   if (p.fmode == kTransposed) {
     // 32 rows of the piece are 32 neighbours of one output row
@@ -254,12 +289,12 @@ __device__ __forceinline__ void emit_user(const Prod& p, const float* v, int g, 
         float* o = static_cast<float*>(p.out) + at;
 #pragma unroll
         for (int q = 0; q < 64; ++q, o += p.um)
-          if (q < left) *o = v[q] * p.f0;
+          if (q < left) *o = v[q] * f;
       } else {
         __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
 #pragma unroll
         for (int q = 0; q < 64; ++q, o += p.um)
-          if (q < left) *o = __float2bfloat16_rn(v[q] * p.f0);
+          if (q < left) *o = __float2bfloat16_rn(v[q] * f);
       }
     }
     return;
@@ -268,7 +303,7 @@ __device__ __forceinline__ void emit_user(const Prod& p, const float* v, int g, 
 #pragma unroll
   for (int u = 0; u < 16; ++u)
     *reinterpret_cast<float4*>(stage + lane * 256 + ((u ^ (lane & 15)) << 4)) =
-        make_float4(v[4 * u] * p.f0, v[4 * u + 1] * p.f0, v[4 * u + 2] * p.f0, v[4 * u + 3] * p.f0);
+        make_float4(v[4 * u] * f, v[4 * u + 1] * f, v[4 * u + 2] * f, v[4 * u + 3] * f);
   __syncwarp();
   auto unit = [&](int r, int u) {
     return *reinterpret_cast<const float4*>(stage + r * 256 + ((u ^ (r & 15)) << 4));
@@ -316,12 +351,11 @@ __device__ __forceinline__ void emit_user(const Prod& p, const float* v, int g, 
   __syncwarp();   // the stage is read before it is written again
 }
 
-// C = A B on 128 CG x 128 CG tiles: CG = 1 one CTA, CG = 2 a CTA pair (cta_group::2, each CTA
-// holds half of the tile's rows of A and half of its columns of B). A is K-major; B is K-major
-// (gram and square: B^T has A's layout) or N-major (update: B = X). Persistent and
-// warp-specialised: warp 0 streams operand tiles by TMA through a ring, one lane of warp 1
-// issues the MMAs into one of two accumulators, warps 4..11 empty the other one (warps 2 and 3
-// complete the first register group).
+// Persistent and warp-specialised. Warp 0 of the leader (rank 0) takes tile numbers from the counter
+// and hands them to the other roles through kSlots slots; warp 0 of every CTA streams operand
+// tiles by TMA through a ring of stages; one lane of the leader's warp 1 issues the MMAs into one
+// of two accumulators; warps 4..11 empty the other one (warps 2 and 3 complete the first register
+// group).
 // The tensor core adds to its fp32 accumulator without rounding to nearest: every 16-deep step
 // loses up to a whole unit in the last place, always towards zero, and K = 2048 in three
 // passes came out 3.8e-5 off. So the parts' small products (hi lo, lo hi) come first, and for fp32
@@ -329,38 +363,39 @@ __device__ __forceinline__ void emit_user(const Prod& p, const float* v, int g, 
 // accumulators in registers (round to nearest) while the next one fills.
 // Every wait is bounded; on expiry the device error word is set, the roles leave their loops,
 // copies and MMAs in flight are waited for (bounded) and TMEM is freed.
-template <int CG, bool B_MN>
+template <typename S>
 __global__ void __launch_bounds__(kThreads, 1)
-ns_product_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_constant__ CUtensorMap tma_b,
-                  const __grid_constant__ CUtensorMap out0, const __grid_constant__ CUtensorMap out1,
-                  const __grid_constant__ CUtensorMap mir0, const __grid_constant__ CUtensorMap mir1,
-                  const __grid_constant__ Prod p) {
-  constexpr int TILE = 128 * CG;
-  constexpr uint32_t TMEM_COLS = 2 * TILE;
+ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
+  constexpr int CG = S::CG, TN = S::TN, STAGES = S::STAGES;
+  constexpr uint32_t TMEM_COLS = 2 * TN;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sa = smem;
-  uint8_t* sb = smem + kStages * kPartBytes;
-  uint8_t* sepi = sb + kStages * kPartBytes;
+  uint8_t* sb = smem + STAGES * S::A_BYTES;
+  uint8_t* sepi = sb + STAGES * S::B_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sepi + kEpiWarps * kEpiStage);
-  uint64_t* full = bars;              // leader only
-  uint64_t* empty = bars + kStages;
-  uint64_t* tfull = empty + kStages;  // [2]
-  uint64_t* tempty = tfull + 2;       // [2], leader only
-  uint64_t* drain = tempty + 2;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* full = bars;                     // [STAGES], leader only
+  uint64_t* empty = full + STAGES;           // [STAGES]
+  uint64_t* tfull = empty + STAGES;          // [2]
+  uint64_t* tempty = tfull + 2;              // [2], leader only
+  uint64_t* wfull = tempty + 2;              // [kSlots]: a tile number is in its slot
+  uint64_t* wempty = wfull + kSlots;         // [kSlots], leader only: every role has read it
+  uint64_t* wready = wempty + kSlots;        // [kSlots]: the product before the tile's is complete
+  uint64_t* aload = wready + kSlots;         // [kEpiWarps]: a warp's tile of A
+  uint64_t* drain = aload + kEpiWarps;
+  volatile int* wtile = reinterpret_cast<volatile int*>(drain + 1);   // [kSlots]
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1) + kSlots;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);   // known to be uniform
+  const int lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
   const bool leader = rank == 0;
-  const Ctl ctl{abort_flag, p.err};
-  const int first = blockIdx.x / CG, step = gridDim.x / CG;
-  const int nk = p.nk * p.nseg;   // K blocks of a tile: p.head, then p.chunk at a time
+  const Ctl ctl{abort_flag, job.err};
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < STAGES; ++s) {
       mbar_init(smem_u32(full + s), 1);
       mbar_init(smem_u32(empty + s), 1);
     }
@@ -368,6 +403,13 @@ ns_product_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_consta
       mbar_init(smem_u32(tfull + a), 1);
       mbar_init(smem_u32(tempty + a), kEpiWarps * CG);
     }
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(smem_u32(wfull + s), 1);
+      mbar_init(smem_u32(wready + s), 1);
+      // the MMA lane, the other CTA's producer, every epilogue warp
+      mbar_init(smem_u32(wempty + s), CG + kEpiWarps * CG);
+    }
+    for (int i = 0; i < kEpiWarps; ++i) mbar_init(smem_u32(aload + i), 1);
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -396,123 +438,207 @@ ns_product_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_consta
   pdl_wait();      // the operands belong to the previous kernel of the stream
   pdl_trigger();
 
+  // Next tile number for a role (a converged warp) other than the leader's producer; job.total or
+  // more: there are no more. n counts the role's tiles.
+  auto take = [&](int n, int& tile) {
+    const int s = n % kSlots;
+    const uint32_t ph = (uint32_t)(n / kSlots) & 1u;
+    const bool ok = wait_inline<CG == 2>(smem_u32(wfull + s), ph, ctl, kErrEpilogue);
+    tile = __shfl_sync(0xffffffffu, wtile[s], 0);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    if (elect_one()) {
+      if constexpr (CG == 2) mbar_arrive_remote(map_to_rank(smem_u32(wempty + s), 0));
+      else mbar_arrive(smem_u32(wempty + s));
+    }
+    return true;
+  };
+
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     if (warp == 0) {
-      // ------------------------------------------------------------ TMA producer
-      if (lane == 0) {
-        int it = 0, s = 0;        // K blocks issued; ring slot and its phase
-        uint32_t ph = 1u;
-        bool ok = true;
-        uint32_t fb0 = smem_u32(full);
-        if constexpr (CG == 2) fb0 = map_to_rank(fb0, 0);
-        for (int tile = first; ok && tile < p.total; tile += step) {
-          const Tile t = decode(p, tile);
-          const int am = t.mb * TILE + (int)rank * 128, bn = t.nb * TILE + (int)rank * 128;
-          for (int seg = 0; ok && seg < p.nseg; ++seg) {
-            const int za = p.pa[seg] * p.batch + t.g, zb = p.pb[seg] * p.batch + t.g;
-            for (int k = 0; k < p.nk * BK; k += BK, ++it) {
-              // stops only when the wait runs out: both CTAs of a pair are released by the same
-              // commits, so both have then issued the same loads
-              if (!wait_inline(smem_u32(empty + s), ph, ctl, kErrProducer, kWaitLimitNs,
-                               /*stop_on_abort=*/false)) {
-                ok = false;
-                break;
-              }
-              const uint32_t fb = fb0 + (uint32_t)(s * 8);
-              if (leader) mbar_expect_tx(smem_u32(full + s), CG * 2 * kPartBytes);
-              load_box<CG>(smem_u32(sa + s * kPartBytes), &tma_a, fb, k, am, za);
-              const uint32_t db = smem_u32(sb + s * kPartBytes);
-              if constexpr (B_MN) {
-                load_box<CG>(db, &tma_b, fb, bn, k, zb);
-                load_box<CG>(db + 64 * BK * 2, &tma_b, fb, bn + 64, k, zb);
-              } else {
-                load_box<CG>(db, &tma_b, fb, k, bn, zb);
-              }
-              if (++s == kStages) { s = 0; ph ^= 1u; }
+      // ------------------------------------------------------------ tile numbers, TMA producer
+      int it = 0, s = 0;        // K blocks issued; ring stage and its phase
+      uint32_t ph = 1u;
+      bool ok = true;
+      uint32_t fb0 = smem_u32(full);
+      if constexpr (CG == 2) fb0 = map_to_rank(fb0, 0);
+      for (int n = 0; ok; ++n) {
+        int tile = 0;
+        if (leader) {
+          // taken when it can be started, not earlier: a number held back by a busy cluster is work
+          // that an idle one does not get
+          if (lane == 0) tile = atomicAdd(job.counter, 1);
+          tile = __shfl_sync(0xffffffffu, tile, 0);
+          const int w = n % kSlots;
+          ok = wait_inline<CG == 2>(smem_u32(wempty + w), ((uint32_t)(n / kSlots) & 1u) ^ 1u, ctl,
+                                    kErrProducer);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (elect_one()) {
+            wtile[w] = tile;
+            mbar_arrive(smem_u32(wfull + w));
+            if constexpr (CG == 2) {
+              asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_rank(
+                               smem_u32(const_cast<int*>(wtile) + w), 1)),
+                           "r"(tile)
+                           : "memory");
+              mbar_arrive_remote(map_to_rank(smem_u32(wfull + w), 1));
             }
           }
+        } else if (!(ok = take(n, tile))) {
+          break;
         }
-        if (!ok && leader)   // let the copies already issued land before the CTA leaves
-          for (int j = max(0, it - kStages); j < it; ++j)
-            wait_inline(smem_u32(full + j % kStages), (uint32_t)(j / kStages) & 1u, ctl, 0,
-                         kDrainLimitNs);
+        if (tile >= job.total) break;
+        const Work w = decode<S>(job, tile);
+        const Kind& k = job.k[w.kind];
+        const int before = w.t * (job.k[0].per + job.k[1].per + job.k[2].per) +
+                           (w.kind > 0 ? job.k[0].per : 0) + (w.kind > 1 ? job.k[1].per : 0);
+        if (before > 0) {
+          // the product before this one is complete for this matrix; then order the loads of the
+          // asynchronous proxy behind that
+          if (lane == 0) ok = wait_done(job.done + w.g, before * kEpiWarps * CG, ctl);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          __syncwarp();
+          asm volatile("fence.proxy.async.global;" ::: "memory");
+        }
+        if (elect_one()) mbar_arrive(smem_u32(wready + n % kSlots));
+        const int x = w.t & 1;
+        const CUtensorMap* ma =
+            w.kind == kGram ? &maps.xa[x] : w.kind == kSquare ? &maps.aa : &maps.ba;
+        const CUtensorMap* mb =
+            w.kind == kGram ? &maps.xb[x] : w.kind == kSquare ? &maps.ab : &maps.xn[x];
+        const int am = w.mb * S::TM + (int)rank * 128, bn = w.nb * TN + (int)rank * S::BN;
+        const int ns = segments(job, w);
+        for (int seg = 0; ok && seg < ns; ++seg) {
+          const int za = part_a(ns, seg) * job.batch + w.g, zb = part_b(ns, seg) * job.batch + w.g;
+          for (int kk = 0; kk < k.nk * BK; kk += BK, ++it) {
+            // stops only when the wait runs out: both CTAs of a pair are released by the same
+            // commits, so both have then issued the same loads
+            ok = wait_inline(smem_u32(empty + s), ph, ctl, kErrProducer, kLimitNs,
+                             /*stop_on_abort=*/false);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            const uint32_t fb = fb0 + (uint32_t)(s * 8);
+            const uint32_t da = smem_u32(sa) + (uint32_t)(s * S::A_BYTES);
+            const uint32_t db = smem_u32(sb) + (uint32_t)(s * S::B_BYTES);
+            if (elect_one()) {
+              if (leader) mbar_expect_tx(smem_u32(full + s), CG * (S::A_BYTES + S::B_BYTES));
+              load_box<CG>(da, ma, fb, kk, am, za);
+              if (w.kind == kUpdate) {
+                load_box<CG>(db, mb, fb, bn, kk, zb);
+                if constexpr (S::BN == 128) load_box<CG>(db + 64 * BK * 2, mb, fb, bn + 64, kk, zb);
+              } else {
+                load_box<CG>(db, mb, fb, kk, bn, zb);
+              }
+            }
+            if (++s == STAGES) { s = 0; ph ^= 1u; }
+          }
+        }
       }
+      if (!ok && leader)   // let the copies already issued land before the CTA leaves
+        for (int j = max(0, it - STAGES); j < it; ++j)
+          wait_inline(smem_u32(full + j % STAGES), (uint32_t)(j / STAGES) & 1u, ctl, 0,
+                      kDrainLimitNs, /*stop_on_abort=*/false);
       __syncwarp();
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
-      if (leader && lane == 0) {
-        constexpr uint32_t id = idesc<CG, B_MN>();
+      if (leader) {
         auto commit = [](uint32_t bar) {
-          if constexpr (CG == 2) umma_commit_pair_both(bar);
-          else umma_commit(bar);
+          if (elect_one()) {
+            if constexpr (CG == 2) umma_commit_pair_both(bar);
+            else umma_commit(bar);
+          }
         };
-        int s = 0, count = 0;   // ring slot, accumulators used
+        int s = 0, count = 0;   // ring stage, accumulators used
         uint32_t ph = 0u;
         bool ok = true;
-        for (int tile = first; ok && tile < p.total; tile += step) {
-          for (int kb = 0, end = p.head; ok && kb < nk; end = min(nk, end + p.chunk), ++count) {
+        for (int n = 0; ok; ++n) {
+          int tile;
+          if (!(ok = take(n, tile)) || tile >= job.total) break;
+          const Work w = decode<S>(job, tile);
+          const int ns = segments(job, w), nk1 = job.k[w.kind].nk, nk = ns * nk1;
+          const bool mn = w.kind == kUpdate;
+          const uint32_t id = idesc<S>() | (mn ? 1u << 16 : 0u);
+          const uint32_t bstep = mn ? 2048u >> 4 : 32u >> 4;
+          const uint32_t a_lo = desc_lo(smem_u32(sa), 16), b_lo = desc_lo(smem_u32(sb), mn ? 64 * BK * 2 : 16);
+          for (int kb = 0, end = head_blocks(job, ns, nk1); ok && kb < nk;
+               end = min(nk, end + kChunk), ++count) {
             const int acc = count & 1;
-            if (!wait_inline(smem_u32(tempty + acc), ((uint32_t)(count >> 1) & 1u) ^ 1u, ctl,
-                             kErrMma)) {
-              ok = false;
-              break;
-            }
+            ok = wait_inline(smem_u32(tempty + acc), ((uint32_t)(count >> 1) & 1u) ^ 1u, ctl, kErrMma);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after();
-            const uint32_t d = tmem_base + (uint32_t)(acc * TILE);
-            for (uint32_t more = 0u; kb < end; ++kb) {
-              if (!wait_inline(smem_u32(full + s), ph, ctl, kErrMma)) {
-                ok = false;
-                break;
-              }
+            const uint32_t d = tmem_base + (uint32_t)(acc * TN);
+            for (uint32_t more = 0u; kb < end; ++kb, more = 1u) {
+              ok = wait_inline(smem_u32(full + s), ph, ctl, kErrMma);
+              if (!(ok = __all_sync(0xffffffffu, ok))) break;
               tc_fence_after();
-              const uint32_t a0 = smem_u32(sa + s * kPartBytes), b0 = smem_u32(sb + s * kPartBytes);
+              const uint32_t a = a_lo + (uint32_t)s * (S::A_BYTES >> 4);
+              const uint32_t b = b_lo + (uint32_t)s * (S::B_BYTES >> 4);
+              if (elect_one()) {
+                mma<CG>(d, a, b, id, more);
 #pragma unroll
-              for (int kk = 0; kk < BK / 16; ++kk, more = 1u) {
-                const uint64_t ad = smem_desc(a0 + kk * 32, 16, 1024);
-                const uint64_t bd = B_MN ? smem_desc(b0 + kk * 2048, 64 * BK * 2, 1024)
-                                         : smem_desc(b0 + kk * 32, 16, 1024);
-                if constexpr (CG == 2) umma_bf16_pair(d, ad, bd, id, more);
-                else umma_bf16(d, ad, bd, id, more);
+                for (int kk = 1; kk < BK / 16; ++kk) mma<CG>(d, a + 2 * kk, b + bstep * kk, id, 1u);
               }
               commit(smem_u32(empty + s));
-              if (++s == kStages) { s = 0; ph ^= 1u; }
+              if (++s == STAGES) { s = 0; ph ^= 1u; }
             }
             if (ok) commit(smem_u32(tfull + acc));
           }
         }
-        commit(smem_u32(drain));   // every MMA of this thread has retired once this completes
-        wait_inline(smem_u32(drain), 0, ctl, ok ? kErrMma : 0, ok ? kWaitLimitNs : kDrainLimitNs);
+        commit(smem_u32(drain));   // every MMA of this lane has retired once this completes
+        wait_inline(smem_u32(drain), 0, ctl, ok ? kErrMma : 0, ok ? kLimitNs : kDrainLimitNs,
+                    /*stop_on_abort=*/false);
       }
       __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ epilogue (warps 4..11)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
-    constexpr int COLS = TILE / 2;        // this warp's columns of the tile
+    constexpr int COLS = S::COLS;         // this warp's columns of the tile
     const int quarter = warp & 3;         // TMEM lanes 32 quarter .. + 31
     const int cbase = ((warp - 4) >> 2) * COLS;
     uint8_t* stage = sepi + (warp - 4) * kEpiStage;
     uint32_t back = smem_u32(tempty);
     if constexpr (CG == 2) back = map_to_rank(back, 0);
-    int count = 0, chunk = 0;
-    bool ok = true;
-    for (int tile = first; ok && tile < p.total; tile += step) {
-      const Tile t = decode(p, tile);
-      const int row0 = t.mb * TILE + (int)rank * 128 + quarter * 32;
-      const bool mirror = p.sym && t.mb != t.nb;
+    uint64_t* abar = aload + (warp - 4);
+    uint32_t aphase = 0;
+    int count = 0;
+    bool ok = true, loading = false;   // (a tile of A is on its way into the stage)
+    for (int n = 0; ok; ++n) {
+      int tile;
+      if (!take(n, tile) || tile >= job.total) break;
+      const Work w = decode<S>(job, tile);
+      const Kind& k = job.k[w.kind];
+      const int ns = segments(job, w), nk = ns * k.nk, head = head_blocks(job, ns, k.nk);
+      const int row0 = w.mb * S::TM + (int)rank * 128 + quarter * 32;
+      const int base0 = w.nb * TN + cbase;
+      // A's 64 columns from c on, for b A, into the stage (which the warp has finished with)
+      auto load_a = [&](int c) {
+        if (lane == 0) {
+          asm volatile("fence.proxy.async;" ::: "memory");
+          const int parts = job.exact ? 2 : 1;
+          mbar_expect_tx(smem_u32(abar), parts * kPiece);
+          for (int part = 0; part < parts; ++part)
+            load_box<1>(smem_u32(stage) + part * kPiece, &maps.as, smem_u32(abar), base0 + c, row0,
+                        part * job.batch + w.g);
+        }
+        loading = true;
+      };
+      if (w.kind == kSquare) {
+        // requested before the accumulators are ready, once A is complete
+        ok = wait_inline(smem_u32(wready + n % kSlots), (uint32_t)(n / kSlots) & 1u, ctl,
+                         kErrDependency);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        load_a(0);
+      }
       float v[COLS];
 #pragma unroll
       for (int q = 0; q < COLS; ++q) v[q] = 0.f;
-      for (int done = 0; done < nk; done = done ? done + p.chunk : p.head, ++count) {
+      for (int done = 0; done < nk; done = done ? done + kChunk : head, ++count) {
         const int acc = count & 1;
-        if (!wait_inline(smem_u32(tfull + acc), (uint32_t)(count >> 1) & 1u, ctl, kErrEpilogue)) {
-          ok = false;
-          break;
-        }
+        ok = wait_inline(smem_u32(tfull + acc), (uint32_t)(count >> 1) & 1u, ctl, kErrEpilogue);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
         const uint32_t trow = tmem_base + ((uint32_t)(quarter * 32) << 16) +
-                              (uint32_t)(acc * TILE + cbase);
+                              (uint32_t)(acc * TN + cbase);
 #pragma unroll
         for (int c = 0; c < COLS; c += 32) {
           uint32_t r[32];
@@ -528,21 +654,73 @@ ns_product_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_consta
         }
       }
       if (!ok) break;
-      // pieces wholly in the padding (or below the diagonal of a packed result) are not stored
-      const int rmax = p.fmode == kToMaps ? p.rows : (int)p.um;
-      const int cmax = p.fmode == kToMaps ? p.cols : (int)p.un;
+      const bool out = w.kind == kUpdate && w.last;
+      const float f = job.f[w.kind][w.t];
+      if (out) {
+#pragma unroll
+        for (int c = 0; c < COLS; c += 64) {
+          // (nothing of a packed result lies below the diagonal)
+          const int col0 = base0 + c;
+          if (row0 < job.um && col0 < job.un && !(job.fmode == kPacked && col0 + 63 <= row0))
+            emit_user(job, v + c, f, w.g, row0, col0, stage, lane);
+        }
+        continue;
+      }
+      if (w.kind == kSquare) {
+        // v <- v f + A fa
+        const float fa = job.fa[w.t];
+#pragma unroll
+        for (int c = 0; c < COLS; c += 64) {
+          if (c > 0) load_a(c);
+          ok = wait_inline(smem_u32(abar), aphase, ctl, kErrDependency);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          aphase ^= 1u;
+          loading = false;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const uint8_t* at = stage + lane * 128 + ((u ^ (lane & 7)) << 4);
+            const uint4 h = *reinterpret_cast<const uint4*>(at);
+            const uint4 l = job.exact ? *reinterpret_cast<const uint4*>(at + kPiece)
+                                      : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float2 a2 = __half22float2(*reinterpret_cast<const __half2*>(&hw[q]));
+              const float2 b2 = __half22float2(*reinterpret_cast<const __half2*>(&lw[q]));
+              float* at2 = v + c + 8 * u + 2 * q;
+              at2[0] = at2[0] * f + (a2.x + b2.x) * fa;
+              at2[1] = at2[1] * f + (a2.y + b2.y) * fa;
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+      const int x = ~w.t & 1;   // X_{t+1}'s buffer
+      const CUtensorMap* to =
+          w.kind == kGram ? &maps.as : w.kind == kSquare ? &maps.bs : &maps.xs[x];
+      const CUtensorMap* to_mirror =
+          w.kind == kGram ? &maps.am : w.kind == kSquare ? &maps.bm : &maps.xm[x];
+      const bool mirror = k.sym && w.nb >= (w.mb + 1) * (S::TM / TN);
+      // bf16 results: the last update reads one part of X
+      const int parts = job.exact || (w.kind == kUpdate && w.t + 2 < job.steps) ? 2 : 1;
 #pragma unroll
       for (int c = 0; c < COLS; c += 64) {
-        const int col0 = t.nb * TILE + cbase + c;
-        if (row0 >= rmax || col0 >= cmax || (p.fmode == kPacked && col0 + 63 <= row0)) continue;
-        if (p.fmode == kToMaps)
-          emit_maps(p, &out0, &out1, &mir0, &mir1, v + c, t.g, row0, col0, mirror,
-                    smem_u32(stage), lane, chunk);
-        else
-          emit_user(p, v + c, t.g, row0, col0, stage, lane);
+        const int col0 = base0 + c;   // pieces wholly in the padding are not stored
+        if (row0 < job.R && col0 < k.cols)
+          emit_maps(to, to_mirror, v + c, w.kind == kSquare ? 1.f : f,
+                    w.kind == kSquare ? job.da[w.t] : 0.f, parts, job.batch, w.g, row0, col0,
+                    mirror, w.kind == kUpdate ? 0x80008000u : 0u, smem_u32(stage), lane);
       }
+      // publish: this warp's copies are complete, then the matrix's count goes up
+      if (lane == 0) {
+        bulk_wait_all();
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        red_release_gpu_add(job.done + w.g, 1);
+      }
+      __syncwarp();
     }
-    if (lane == 0) bulk_wait_all();   // every store written before the CTA leaves
+    if (loading) wait_inline(smem_u32(abar), aphase, ctl, 0, kDrainLimitNs, /*stop_on_abort=*/false);
     __syncwarp();
   }
 
@@ -563,7 +741,6 @@ ns_product_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_consta
 }
 
 // ------------------------------------------------------------------ norm and first split
-constexpr int kNormThreads = 256;
 constexpr int64_t kNormChunk = 16384;   // elements per block of the norm pass, at least
 constexpr int kMaxChunks = 512;
 
@@ -571,31 +748,15 @@ int norm_chunks(int64_t elems) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxChunks, elems / kNormChunk));
 }
 
-__device__ __forceinline__ float ld_in(const void* p, long long i, int f32) {
-  return f32 ? static_cast<const float*>(p)[i]
-             : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
-
-__device__ __forceinline__ double block_sum(double v) {
-  __shared__ double part[kNormThreads / 32];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  double s = 0.0;
-#pragma unroll
-  for (int w = 0; w < kNormThreads / 32; ++w) s += part[w];
-  __syncthreads();
-  return s;
-}
-
 // partial[g][chunk] = sum of the chunk's squares, in 64 bits: an fp32 square overflows at 1.8e19
 // and vanishes at 1e-23, both of which are ordinary fp32 and bf16 values.
 __global__ void __launch_bounds__(kNormThreads)
 ns_norm_kernel(const void* __restrict__ x, int f32, long long elems, int chunks,
-               double* __restrict__ partial) {
+               double* __restrict__ partial, int* __restrict__ counts, int ncounts) {
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.x == 0 && blockIdx.y == 0)   // the products' counters start at zero
+    for (int i = threadIdx.x; i < ncounts; i += kNormThreads) counts[i] = 0;
   const long long base = (long long)blockIdx.y * elems;
   const long long per = (elems + chunks - 1) / chunks;
   const long long lo = per * blockIdx.x, hi = min(elems, lo + per);
@@ -701,21 +862,6 @@ bool make_map3(CUtensorMap* m, const void* base, int64_t mats, int64_t rows, int
             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A workspace stack and the ways the products address it.
-struct Stack {
-  __half* base = nullptr;
-  int64_t rows = 0, cols = 0;
-  CUtensorMap k, mn, st, mir;   // K-major operand, N-major operand, store, mirrored store
-  bool init(__half* b, int64_t mats, int64_t r, int64_t c) {
-    base = b; rows = r; cols = c;
-    constexpr CUtensorMapSwizzle k128 = CU_TENSOR_MAP_SWIZZLE_128B, k64 = CU_TENSOR_MAP_SWIZZLE_64B;
-    return make_map3(&k, b, mats, r, c, 64, 128, k128) &&
-           make_map3(&mn, b, mats, r, c, 64, 64, k128) &&
-           make_map3(&st, b, mats, r, c, 64, 32, k128) &&
-           make_map3(&mir, b, mats, r, c, 32, 64, k64);
-  }
-};
-
 struct Dims {
   int64_t r, k, R, ld;
   bool tall;
@@ -736,19 +882,20 @@ Dims dims_of(const Problem& p) {
 
 struct Ws {
   double* partial;
-  __half *x[2], *a, *h, *b;
+  int* counts;              // tiles handed out, then one count per matrix
+  __half *x[2], *a, *b;
 };
 size_t layout(const Problem& p, void* base, Ws* o) {
   const Dims d = dims_of(p);
   Arena ar(base, SIZE_MAX);
   Ws w;
   w.partial = static_cast<double*>(ar.take((size_t)p.batch * d.chunks * sizeof(double)));
+  w.counts = static_cast<int*>(ar.take((size_t)(p.batch + 1) * sizeof(int)));
   const size_t xb = (size_t)(2 * p.batch * d.R * d.ld) * 2;
   const size_t gb = (size_t)(2 * p.batch * d.R * d.R) * 2;
   w.x[0] = static_cast<__half*>(ar.take(xb));
   w.x[1] = p.steps > 1 ? static_cast<__half*>(ar.take(xb)) : nullptr;
   w.a = static_cast<__half*>(ar.take(gb));
-  w.h = static_cast<__half*>(ar.take(gb));
   w.b = static_cast<__half*>(ar.take(gb));
   if (o) *o = w;
   return ar.used;
@@ -761,11 +908,64 @@ int sm_total() {
   return n > 0 ? n : 148;
 }
 
-template <int CG, bool B_MN>
-cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const Stack* o0, const Stack* o1,
-                   const Prod& p, int sms, const char* name, cudaStream_t s) {
-  auto kern = ns_product_kernel<CG, B_MN>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+Kind kind_of(int64_t rows, int64_t cols, int64_t K, int tm, int tn, bool sym) {
+  Kind k;
+  k.tiles_m = (int)((rows + tm - 1) / tm);
+  k.tiles_n = (int)((cols + tn - 1) / tn);
+  k.sym = sym;
+  k.cols = (int)cols;
+  k.nk = (int)(K / BK);
+  k.per = k.tiles_m * k.tiles_n;
+  if (sym) {
+    k.per = 0;
+    for (int i = 0; i < k.tiles_m; ++i) k.per += k.tiles_n - tm / tn * i;
+  }
+  return k;
+}
+
+// Tile shape and use of symmetry of a problem.
+struct Choice {
+  int cg, tn;
+  bool sym;
+};
+// The fastest of them by a model of one step: the work of all matrices shared out over the GPU, and
+// one matrix's three products one after the other, each in whole waves of tiles; the longer of the
+// two and a quarter of the other. Rates as measured (us): a 64-deep K block of a 256 x 256, 256 x
+// 128 (CTA pair) or 128 x 128 tile (one CTA) 0.31, 0.26, 0.26 in a chain, 0.33, 0.35, 0.33 with
+// every SM busy (small tiles are then bound by L2); 64 columns of an epilogue warp on their way
+// out 1 per part, 2.2 if mirrored; 3 from a product's last store to the next one's first load.
+// Measured against the other choices (in one run each): 8B up bf16 256 x 256 symmetric 4.4 ms,
+// full 5.5, 256 x 128 5.6; 36 blocks of 512 128 x 128 symmetric 398 us, 256 x 256 425, 256 x 128 467;
+// 3 of 1000 x 333 256 x 128 full 229, symmetric 248, 256 x 256 383; 4096 x 1024 bf16 263 against 311.
+Choice choose(const Problem& p, const Dims& d, int sms) {
+  const bool exact = p.out_t == DT::F32, skew = p.form == Form::Skew;
+  if (d.R <= 128) return {1, 128, false};   // one row of tiles: nothing to mirror
+  Choice best{2, 256, true};
+  double best_t = 1e30;
+  for (const Choice c : {Choice{2, 256, true}, Choice{2, 128, true}, Choice{2, 256, false},
+                         Choice{2, 128, false}, Choice{1, 128, true}, Choice{1, 128, false}}) {
+    const int tm = 128 * c.cg, workers = sms / c.cg;
+    const double busy_us = c.tn == 256 || c.cg == 1 ? 0.33 : 0.35;
+    const double block_us = c.tn == 256 ? 0.31 : 0.26;
+    double work = 0.0, chain = 0.0;
+    for (int kind = 0; kind < 3; ++kind) {
+      const bool sym = c.sym && (kind < 2 || skew);
+      const Kind k = kind_of(d.R, kind < 2 ? d.R : d.ld, kind == 0 ? d.ld : d.R, tm, c.tn, sym);
+      const int blocks = k.nk * (exact ? 3 : kind == 2 ? 2 : 1);
+      const double out = c.tn / 128 * (exact || kind == 2 ? 2 : 1) * (sym ? 2.2 : 1.0);
+      work += (double)p.batch * k.per * std::max(blocks * busy_us, out) / workers;
+      chain += std::ceil((double)k.per / workers) * blocks * block_us + out + 3.0;
+    }
+    const double t = std::max(work, chain) + 0.25 * std::min(work, chain);
+    if (t < best_t) { best_t = t; best = c; }
+  }
+  return best;
+}
+
+template <typename S>
+cudaError_t launch(const Maps& maps, const Job& job, int sms, cudaStream_t s) {
+  auto kern = ns_kernel<S>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
   if (e != cudaSuccess) return e;
   // setmaxnreg waits for registers that the block was not launched with: refuse such a build
   static const int regs = [kern] {
@@ -777,19 +977,20 @@ cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const Stack* o0, 
   cudaLaunchAttribute attr[2];
   set_pdl_attr(attr[0]);
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.x = S::CG;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)(CG * std::min(p.total, sms / CG)));
+  // as many clusters as one product of all matrices has tiles, at most one CTA per SM
+  int most = 0;
+  for (const Kind& k : job.k) most = std::max(most, k.per * job.batch);
+  cfg.gridDim = dim3((unsigned)(S::CG * std::min(most, sms / S::CG)));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = S::SMEM;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = CG == 2 ? 2 : 1;
-  TraceScope t(name, s);
-  const CUtensorMap& s0 = o0 ? o0->st : a;
-  const CUtensorMap& m0 = o0 ? o0->mir : a;
-  return cudaLaunchKernelEx(&cfg, kern, a, b, s0, o1 ? o1->st : s0, m0, o1 ? o1->mir : m0, p);
+  cfg.numAttrs = S::CG == 2 ? 2 : 1;
+  TraceScope t("ns_products", s);
+  return cudaLaunchKernelEx(&cfg, kern, maps, job);
 }
 
 }  // namespace
@@ -810,20 +1011,18 @@ bool make_plan(const float* coeffs, int steps, Plan* plan) {
   for (int t = 0; t < steps; ++t) {
     const double a = coeffs[3 * t], b = coeffs[3 * t + 1], c = coeffs[3 * t + 2];
     if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
-    double h = 0.0, bb = 0.0, x = 0.0;
+    double bb = 0.0, x = 0.0;
     for (int i = 0; i <= kSamples; ++i) {
       const double s = top * i / kSamples, l = s * s;
-      h = std::max(h, std::fabs(b + c * l));
       bb = std::max(bb, std::fabs(a + b * l + c * l * l));
       x = std::max(x, s * std::fabs(a + b * l + c * l * l));
     }
     // entries of a matrix do not pass its spectral norm; 2 % for the samples and the rounding
     plan->sx[t] = pow2_scale(1.02 * top);
     plan->sa[t] = pow2_scale(1.02 * top * top);
-    plan->sh[t] = pow2_scale(1.02 * h);
     plan->sb[t] = pow2_scale(1.02 * bb);
     top = 1.02 * x;
-    if (!(top < 1e6) || !(h < 1e12) || !(bb < 1e12)) return false;
+    if (!(top < 1e6) || !(bb < 1e12)) return false;
   }
   plan->sx[steps] = 1.f;
   return true;
@@ -845,7 +1044,7 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
     TraceScope t("ns_norm", s);
     cudaError_t e = launch_k(ns_norm_kernel, dim3((unsigned)d.chunks, (unsigned)p.batch),
                              dim3(kNormThreads), 0, s, x, in_f32, (long long)d.elems, d.chunks,
-                             w.partial);
+                             w.partial, w.counts, (int)p.batch + 1);
     if (e != cudaSuccess) return e;
   }
   {
@@ -861,86 +1060,69 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
                              dim3(256), 0, s, q);
     if (e != cudaSuccess) return e;
   }
-  Stack X[2], A, H, B;
-  const int64_t mats = 2 * p.batch;
-  if (!X[0].init(w.x[0], mats, d.R, d.ld) || (w.x[1] && !X[1].init(w.x[1], mats, d.R, d.ld)) ||
-      !A.init(w.a, mats, d.R, d.R) || !H.init(w.h, mats, d.R, d.R) || !B.init(w.b, mats, d.R, d.R))
-    return cudaErrorInvalidValue;
-
   const int sms = sm_total();
-  // 256-wide pair tiles need half the operand traffic per product of 128-wide ones, which
-  // fill the GPU with a quarter of the work
-  auto tiles = [&](int64_t rows, int64_t cols, int tile, bool sym) {
-    const int64_t tm = (rows + tile - 1) / tile, tn = (cols + tile - 1) / tile;
-    return (sym ? tm * (tm + 1) / 2 : tm * tn) * p.batch;
-  };
-  auto product = [&](const CUtensorMap& a, const CUtensorMap& b, bool b_mn, int64_t cols, int64_t K,
-                     bool sym, Prod q, const Stack* o0, const Stack* o1, const char* name) {
-    const int64_t rows = d.R;
-    const bool pair = tiles(rows, cols, 256, sym) >= sms / 4 && rows > 128;
-    const int tile = pair ? 256 : 128;
-    q.batch = (int)p.batch;
-    q.tiles_m = (int)((rows + tile - 1) / tile);
-    q.tiles_n = (int)((cols + tile - 1) / tile);
-    q.sym = sym;
-    q.per = (int)(tiles(rows, cols, tile, sym) / p.batch);
-    q.total = (int)tiles(rows, cols, tile, sym);
-    q.rows = (int)rows; q.cols = (int)cols;
-    q.nk = (int)(K / BK);
-    // the small products and the first of the large ones in one accumulator
-    q.head = exact ? (q.nseg - 1) * q.nk + std::min(kChunk, q.nk) : q.nk * q.nseg;
-    q.chunk = kChunk;
-    q.err = err;
-    if (b_mn)
-      return pair ? launch<2, true>(a, b, o0, o1, q, sms, name, s)
-                  : launch<1, true>(a, b, o0, o1, q, sms, name, s);
-    return pair ? launch<2, false>(a, b, o0, o1, q, sms, name, s)
-                : launch<1, false>(a, b, o0, o1, q, sms, name, s);
-  };
-  auto segments = [](Prod& q, int n) {
-    // hi hi | hi lo, hi hi | lo hi, hi lo, hi hi: small products first
-    q.nseg = n;
-    const int pa[3] = {1, 0, 0}, pb[3] = {0, 1, 0};
-    for (int i = 0; i < n; ++i) { q.pa[i] = pa[3 - n + i]; q.pb[i] = pb[3 - n + i]; }
-  };
+  const Choice c = choose(p, d, sms);
+  const int tm = 128 * c.cg, bn = c.tn / c.cg;
 
-  for (int t = 0; t < p.steps; ++t) {
-    const float* c = p.coeffs + 3 * t;
-    const bool last = t + 1 == p.steps;
-    const double sx = plan.sx[t], sa = plan.sa[t], sh = plan.sh[t], sb = plan.sb[t];
-    const Stack& Xt = X[t & 1];
-    Prod q{};
-    segments(q, exact ? 3 : 1);
-    q.lo = exact; q.mirror = 1.f; q.has1 = 1;
-    q.f0 = (float)(sa / (sx * sx)); q.d0 = 0.f;
-    q.f1 = (float)(sh * c[2] / (sx * sx)); q.d1 = (float)(sh * c[1]);
-    cudaError_t e = product(Xt.k, Xt.k, false, d.R, d.ld, true, q, &A, &H, "ns_gram");
-    if (e != cudaSuccess) return e;
-
-    q.has1 = 0;
-    q.f0 = (float)(sb / (sa * sh)); q.d0 = (float)(sb * c[0]);
-    e = product(A.k, H.k, false, d.R, d.R, true, q, &B, nullptr, "ns_square");
-    if (e != cudaSuccess) return e;
-
-    q.d0 = 0.f;
-    segments(q, exact ? 3 : (last ? 1 : 2));
-    if (!last) {
-      q.f0 = (float)(plan.sx[t + 1] / (sb * sx));
-      q.lo = exact || t + 2 < p.steps;   // the last bf16 update reads one part
-      q.mirror = -1.f;
-      const Stack& Xn = X[(t + 1) & 1];
-      e = product(B.k, Xt.mn, true, d.ld, d.R, skew, q, &Xn, nullptr, "ns_update");
-    } else {
-      q.f0 = (float)(p.scale / (sb * sx));
-      q.fmode = skew ? kPacked : d.tall ? kTransposed : kRows;
-      q.out = out; q.out_f32 = exact;
-      q.um = d.r; q.un = d.k;
-      q.vec = (d.k * (exact ? 4 : 2)) % 16 == 0;
-      e = product(B.k, Xt.mn, true, d.ld, d.R, skew, q, nullptr, nullptr, "ns_update_out");
-    }
-    if (e != cudaSuccess) return e;
+  Maps maps{};
+  const int64_t mats = 2 * p.batch;
+  constexpr CUtensorMapSwizzle k128 = CU_TENSOR_MAP_SWIZZLE_128B, k64 = CU_TENSOR_MAP_SWIZZLE_64B;
+  bool ok = true;
+  for (int i = 0; i < 2; ++i) {
+    if (!w.x[i]) continue;
+    ok = ok && make_map3(&maps.xa[i], w.x[i], mats, d.R, d.ld, 64, 128, k128) &&
+         make_map3(&maps.xb[i], w.x[i], mats, d.R, d.ld, 64, bn, k128) &&
+         make_map3(&maps.xn[i], w.x[i], mats, d.R, d.ld, 64, 64, k128) &&
+         make_map3(&maps.xs[i], w.x[i], mats, d.R, d.ld, 64, 32, k128) &&
+         make_map3(&maps.xm[i], w.x[i], mats, d.R, d.ld, 32, 64, k64);
   }
-  return cudaSuccess;
+  ok = ok && make_map3(&maps.aa, w.a, mats, d.R, d.R, 64, 128, k128) &&
+       make_map3(&maps.ab, w.a, mats, d.R, d.R, 64, bn, k128) &&
+       make_map3(&maps.as, w.a, mats, d.R, d.R, 64, 32, k128) &&
+       make_map3(&maps.am, w.a, mats, d.R, d.R, 32, 64, k64) &&
+       make_map3(&maps.ba, w.b, mats, d.R, d.R, 64, 128, k128) &&
+       make_map3(&maps.bs, w.b, mats, d.R, d.R, 64, 32, k128) &&
+       make_map3(&maps.bm, w.b, mats, d.R, d.R, 32, 64, k64);
+  if (!ok) return cudaErrorInvalidValue;
+
+  Job job{};
+  job.k[kGram] = kind_of(d.R, d.R, d.ld, tm, c.tn, c.sym);
+  job.k[kSquare] = kind_of(d.R, d.R, d.R, tm, c.tn, c.sym);
+  job.k[kUpdate] = kind_of(d.R, d.ld, d.R, tm, c.tn, c.sym && skew);
+  job.batch = (int)p.batch;
+  job.steps = p.steps;
+  int64_t per_step = 0;
+  for (const Kind& k : job.k) per_step += (int64_t)k.per * p.batch;
+  // the counts reach 16 per tile
+  if (per_step * p.steps * 16 > INT32_MAX) return cudaErrorInvalidValue;
+  job.per_step = (int)per_step;
+  job.total = job.per_step * p.steps;
+  job.R = (int)d.R;
+  job.exact = exact;
+  job.skew = skew;
+  job.fmode = skew ? kPacked : d.tall ? kTransposed : kRows;
+  job.out = out;
+  job.out_f32 = exact;
+  job.um = d.r;
+  job.un = d.k;
+  job.vec = (d.k * (exact ? 4 : 2)) % 16 == 0;
+  job.counter = w.counts;
+  job.done = w.counts + 1;
+  job.err = err;
+  for (int t = 0; t < p.steps; ++t) {
+    // stored: X sx, A sa, B sb
+    const float* q = p.coeffs + 3 * t;
+    const double sx = plan.sx[t], sa = plan.sa[t], sb = plan.sb[t];
+    const double next = t + 1 < p.steps ? plan.sx[t + 1] : p.scale;
+    job.f[kGram][t] = (float)(sa / (sx * sx));
+    job.f[kSquare][t] = (float)(sb * q[2] / (sa * sa));
+    job.fa[t] = (float)(sb * q[1] / sa);
+    job.da[t] = (float)(sb * q[0]);
+    job.f[kUpdate][t] = (float)(next / (sb * sx));
+  }
+  if (c.cg == 1) return launch<Shape<1, 128>>(maps, job, sms, s);
+  return c.tn == 256 ? launch<Shape<2, 256>>(maps, job, sms, s)
+                     : launch<Shape<2, 128>>(maps, job, sms, s);
 }
 
 }  // namespace orth

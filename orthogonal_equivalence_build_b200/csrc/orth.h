@@ -25,7 +25,7 @@ struct Problem {
 // Powers of two that hold every operand of every step inside fp16 (see orth.cu).
 struct Plan {
   float sx[kMaxSteps + 1];   // scale of X before step t
-  float sa[kMaxSteps], sh[kMaxSteps], sb[kMaxSteps];
+  float sa[kMaxSteps], sb[kMaxSteps];   // of A and B
 };
 // false: the coefficients are not finite or let the singular values grow past every bound
 bool make_plan(const float* coeffs, int steps, Plan* plan);
