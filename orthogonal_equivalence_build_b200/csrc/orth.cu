@@ -1028,10 +1028,25 @@ bool make_plan(const float* coeffs, int steps, Plan* plan) {
   return true;
 }
 
+void fill_factors(const Problem& p, const Plan& plan, float (*f)[kMaxSteps], float* fa, float* da) {
+  for (int t = 0; t < p.steps; ++t) {
+    // stored: X sx, A sa, B sb
+    const float* q = p.coeffs + 3 * t;
+    const double sx = plan.sx[t], sa = plan.sa[t], sb = plan.sb[t];
+    const double next = t + 1 < p.steps ? plan.sx[t + 1] : p.scale;
+    f[0][t] = (float)(sa / (sx * sx));
+    f[1][t] = (float)(sb * q[2] / (sa * sa));
+    fa[t] = (float)(sb * q[1] / sa);
+    da[t] = (float)(sb * q[0]);
+    f[2][t] = (float)(next / (sb * sx));
+  }
+}
+
 size_t workspace_bytes(const Problem& p) { return layout(p, nullptr, nullptr); }
 
 cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, void* ws,
                 cudaStream_t s) {
+  if (small_fits(p)) return run_small(p, plan, x, out, s);
   const Dims d = dims_of(p);
   Ws w;
   layout(p, ws, &w);
@@ -1109,17 +1124,7 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
   job.counter = w.counts;
   job.done = w.counts + 1;
   job.err = err;
-  for (int t = 0; t < p.steps; ++t) {
-    // stored: X sx, A sa, B sb
-    const float* q = p.coeffs + 3 * t;
-    const double sx = plan.sx[t], sa = plan.sa[t], sb = plan.sb[t];
-    const double next = t + 1 < p.steps ? plan.sx[t + 1] : p.scale;
-    job.f[kGram][t] = (float)(sa / (sx * sx));
-    job.f[kSquare][t] = (float)(sb * q[2] / (sa * sa));
-    job.fa[t] = (float)(sb * q[1] / sa);
-    job.da[t] = (float)(sb * q[0]);
-    job.f[kUpdate][t] = (float)(next / (sb * sx));
-  }
+  fill_factors(p, plan, job.f, job.fa, job.da);
   if (c.cg == 1) return launch<Shape<1, 128>>(maps, job, sms, s);
   return c.tn == 256 ? launch<Shape<2, 256>>(maps, job, sms, s)
                      : launch<Shape<2, 128>>(maps, job, sms, s);

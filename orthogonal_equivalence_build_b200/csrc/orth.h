@@ -30,6 +30,15 @@ struct Plan {
 // false: the coefficients are not finite or let the singular values grow past every bound
 bool make_plan(const float* coeffs, int steps, Plan* plan);
 
+// Factors of the epilogues: gram, square and update results are f[0..2][t] times the accumulator;
+// square adds fa[t] A and da[t] I (operands as stored, scales included).
+void fill_factors(const Problem& p, const Plan& plan, float (*f)[kMaxSteps], float* fa, float* da);
+
+// One CTA per matrix (orth_small.cu), where a matrix fits into shared memory.
+bool small_fits(const Problem& p);
+cudaError_t run_small(const Problem& p, const Plan& plan, const void* x, void* out,
+                      cudaStream_t s);
+
 size_t workspace_bytes(const Problem& p);
 cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, void* ws,
                 cudaStream_t s);
