@@ -751,30 +751,53 @@ int norm_chunks(int64_t elems) {
 // partial[g][chunk] = sum of the chunk's squares, in 64 bits: an fp32 square overflows at 1.8e19
 // and vanishes at 1e-23, both of which are ordinary fp32 and bf16 values.
 __global__ void __launch_bounds__(kNormThreads)
-ns_norm_kernel(const void* __restrict__ x, int f32, long long elems, int chunks,
+ns_norm_kernel(const void* __restrict__ x, int f32, int vec, long long elems, int chunks,
                double* __restrict__ partial, int* __restrict__ counts, int ncounts) {
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x == 0 && blockIdx.y == 0)   // the products' counters start at zero
     for (int i = threadIdx.x; i < ncounts; i += kNormThreads) counts[i] = 0;
   const long long base = (long long)blockIdx.y * elems;
-  const long long per = (elems + chunks - 1) / chunks;
-  const long long lo = per * blockIdx.x, hi = min(elems, lo + per);
+  const long long per = ((elems + chunks - 1) / chunks + 7) / 8 * 8;
+  const long long lo = min(elems, per * blockIdx.x), hi = min(elems, lo + per);
   double s = 0.0;
-  for (long long i = lo + threadIdx.x; i < hi; i += kNormThreads) {
-    const double v = ld_in(x, base + i, f32);
-    s += v * v;
+  if (vec) {   // every matrix, and so every range, starts on 16 bytes
+    if (f32) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + base);
+#pragma unroll 4
+      for (long long i = lo / 4 + threadIdx.x; i < hi / 4; i += kNormThreads) {
+        const float4 v = __ldg(p + i);
+        s += (double)v.x * v.x + (double)v.y * v.y + (double)v.z * v.z + (double)v.w * v.w;
+      }
+    } else {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) + base);
+#pragma unroll 4
+      for (long long i = lo / 8 + threadIdx.x; i < hi / 8; i += kNormThreads) {
+        const uint4 v = __ldg(p + i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const double a = __uint_as_float(w[k] << 16), b = __uint_as_float(w[k] & 0xffff0000u);
+          s += a * a + b * b;
+        }
+      }
+    }
+  } else {
+    for (long long i = lo + threadIdx.x; i < hi; i += kNormThreads) {
+      const double v = ld_in(x, base + i, f32);
+      s += v * v;
+    }
   }
   s = block_sum(s);
   if (threadIdx.x == 0) partial[(long long)blockIdx.y * chunks + blockIdx.x] = s;
 }
 
-// X_0 in two fp16 parts, [2][batch][R][ld], from the caller's array, one 64 x 64 tile per block:
-// the tile goes through shared memory, so that reads follow the caller's rows and writes the
-// workspace's, whichever way round they are. Padding is written as zeros.
+// X_0 in two fp16 parts, [2][batch][R][ld], from the caller's array: eight values at a time where
+// the caller's rows are the workspace's, else by 64 x 64 tiles through shared memory, so that reads
+// follow the caller's rows and writes the workspace's. Padding is written as zeros.
 struct Prep {
   const void* x;
-  int f32, form, tall, chunks, batch, tiles_c;
+  int f32, form, tall, vec, chunks, batch, tiles, tiles_c;
   long long m, n;            // the caller's matrix (Skew: m = n = b)
   int r, k, R, ld;           // the workspace's: r x k in R x ld
   double eps, sx, norm_mult; // norm^2 = norm_mult * sum of the partials
@@ -790,38 +813,14 @@ __global__ void __launch_bounds__(256) ns_prep_kernel(const __grid_constant__ Pr
   for (int c = tid; c < p.chunks; c += 256) s += p.partial[(long long)g * p.chunks + c];
   s = block_sum(s);
   const double f = p.sx / (sqrt(p.norm_mult * s) + p.eps);
-  const int tr = blockIdx.x / p.tiles_c, tc = blockIdx.x - tr * p.tiles_c;
-  if (p.form == (int)Form::Skew && tr > tc) return;   // written by its mirror
-  const int i0 = tr * 64, j0 = tc * 64;
-#pragma unroll 4
-  for (int e = tid; e < 4096; e += 256) {
-    const int u = e >> 6, w = e & 63;     // w runs along the caller's rows
-    float v = 0.f;
-    if (p.form == (int)Form::Skew) {
-      const int i = i0 + u, j = j0 + w;
-      if (i < j && j < p.r)
-        v = (float)((double)ld_in(p.x, (long long)g * (p.m * (p.m - 1) / 2) + i * p.m -
-                                           (long long)i * (i + 1) / 2 - i - 1 + j, 1) * f);
-      tile[u][w] = v;
-    } else if (!p.tall) {
-      if (i0 + u < p.r && j0 + w < p.k)
-        v = (float)((double)ld_in(p.x, ((long long)g * p.m + i0 + u) * p.n + j0 + w, p.f32) * f);
-      tile[u][w] = v;
-    } else {   // the caller's row is a workspace column
-      if (j0 + u < p.k && i0 + w < p.r)
-        v = (float)((double)ld_in(p.x, ((long long)g * p.m + j0 + u) * p.n + i0 + w, p.f32) * f);
-      tile[w][u] = v;
-    }
-  }
-  __syncthreads();
-  const bool diag = tr == tc;
   const long long part = (long long)p.batch * p.R * p.ld;
   auto store8 = [&](int i, int j, const float (&v)[8]) {
     uint32_t h[4], l[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const __half2 a = __floats2half2_rn(v[2 * q], v[2 * q + 1]);
-      const __half2 b = __floats2half2_rn(v[2 * q] - __low2float(a), v[2 * q + 1] - __high2float(a));
+      const __half2 b =
+          __floats2half2_rn(v[2 * q] - __low2float(a), v[2 * q + 1] - __high2float(a));
       h[q] = *reinterpret_cast<const uint32_t*>(&a);
       l[q] = *reinterpret_cast<const uint32_t*>(&b);
     }
@@ -829,20 +828,79 @@ __global__ void __launch_bounds__(256) ns_prep_kernel(const __grid_constant__ Pr
     *reinterpret_cast<uint4*>(at) = make_uint4(h[0], h[1], h[2], h[3]);
     *reinterpret_cast<uint4*>(at + part) = make_uint4(l[0], l[1], l[2], l[3]);
   };
+  if (p.vec) {   // the caller's rows are the workspace's and start on 16 bytes
+    const int per_row = p.ld / 8, total = p.R * per_row;
+#pragma unroll 2
+    for (int e = blockIdx.x * 256 + tid; e < total; e += gridDim.x * 256) {
+      const int i = e / per_row, j = (e - i * per_row) * 8;
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (i < p.r) {
+        const long long at = ((long long)g * p.m + i) * p.n + j;
+        if (p.f32) {
 #pragma unroll
-  for (int e = tid; e < 512; e += 256) {
-    const int u = e >> 3, w = (e & 7) * 8;
-    float v[8];
+          for (int q = 0; q < 8; q += 4)
+            if (j + q < p.k) {
+              const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(p.x) + at + q);
+              v[q] = x.x; v[q + 1] = x.y; v[q + 2] = x.z; v[q + 3] = x.w;
+            }
+        } else if (j < p.k) {
+          const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.x) + at);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      v[q] = tile[u][w + q];
-      if (p.form == (int)Form::Skew && diag && u > w + q) v[q] = -tile[w + q][u];
+          for (int q = 0; q < 4; ++q) {
+            v[2 * q] = __uint_as_float(w[q] << 16);
+            v[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
+          }
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = (float)((double)v[q] * f);
+      store8(i, j, v);
     }
-    store8(i0 + u, j0 + w, v);   // R and ld are multiples of 64
-    if (p.form == (int)Form::Skew && !diag) {
+    return;
+  }
+  for (int t = blockIdx.x; t < p.tiles; t += gridDim.x) {
+    const int tr = t / p.tiles_c, tc = t - tr * p.tiles_c;
+    if (p.form == (int)Form::Skew && tr > tc) continue;   // written by its mirror
+    const int i0 = tr * 64, j0 = tc * 64;
+    __syncthreads();   // the tile before has been stored
+#pragma unroll 4
+    for (int e = tid; e < 4096; e += 256) {
+      const int u = e >> 6, w = e & 63;     // w runs along the caller's rows
+      float v = 0.f;
+      if (p.form == (int)Form::Skew) {
+        const int i = i0 + u, j = j0 + w;
+        if (i < j && j < p.r)
+          v = (float)((double)ld_in(p.x, (long long)g * (p.m * (p.m - 1) / 2) + i * p.m -
+                                             (long long)i * (i + 1) / 2 - i - 1 + j, 1) * f);
+        tile[u][w] = v;
+      } else if (!p.tall) {
+        if (i0 + u < p.r && j0 + w < p.k)
+          v = (float)((double)ld_in(p.x, ((long long)g * p.m + i0 + u) * p.n + j0 + w, p.f32) * f);
+        tile[u][w] = v;
+      } else {   // the caller's row is a workspace column
+        if (j0 + u < p.k && i0 + w < p.r)
+          v = (float)((double)ld_in(p.x, ((long long)g * p.m + j0 + u) * p.n + i0 + w, p.f32) * f);
+        tile[w][u] = v;
+      }
+    }
+    __syncthreads();
+    const bool diag = tr == tc;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = -tile[w + q][u];
-      store8(j0 + u, i0 + w, v);
+    for (int e = tid; e < 512; e += 256) {
+      const int u = e >> 3, w = (e & 7) * 8;
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        v[q] = tile[u][w + q];
+        if (p.form == (int)Form::Skew && diag && u > w + q) v[q] = -tile[w + q][u];
+      }
+      store8(i0 + u, j0 + w, v);   // R and ld are multiples of 64
+      if (p.form == (int)Form::Skew && !diag) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = -tile[w + q][u];
+        store8(j0 + u, i0 + w, v);
+      }
     }
   }
 }
@@ -1006,20 +1064,35 @@ float pow2_scale(double most) {
 }  // namespace
 
 bool make_plan(const float* coeffs, int steps, Plan* plan) {
-  constexpr int kSamples = 4096;
   double top = 1.0;   // the singular values of X lie in [0, top]
   for (int t = 0; t < steps; ++t) {
     const double a = coeffs[3 * t], b = coeffs[3 * t + 1], c = coeffs[3 * t + 2];
     if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
-    double bb = 0.0, x = 0.0;
-    for (int i = 0; i <= kSamples; ++i) {
-      const double s = top * i / kSamples, l = s * s;
-      bb = std::max(bb, std::fabs(a + b * l + c * l * l));
-      x = std::max(x, s * std::fabs(a + b * l + c * l * l));
+    // With l = s^2: B's eigenvalues a + b l + c l^2 and the next singular values
+    // s |a + b l + c l^2| over l in [0, top^2] have their extremes at the ends or where the
+    // derivatives b + 2 c l and a + 3 b l + 5 c l^2 vanish.
+    const double end = top * top;
+    double bb = std::fabs(a), x = 0.0;
+    auto look = [&](double l) {
+      if (!(l > 0.0 && l <= end)) return;
+      const double e = std::fabs(a + b * l + c * l * l);
+      bb = std::max(bb, e);
+      x = std::max(x, std::sqrt(l) * e);
+    };
+    look(end);
+    if (c != 0.0) {
+      look(-b / (2.0 * c));
+      const double disc = 9.0 * b * b - 20.0 * a * c;
+      if (disc >= 0.0) {
+        look((-3.0 * b + std::sqrt(disc)) / (10.0 * c));
+        look((-3.0 * b - std::sqrt(disc)) / (10.0 * c));
+      }
+    } else if (b != 0.0) {
+      look(-a / (3.0 * b));
     }
-    // entries of a matrix do not pass its spectral norm; 2 % for the samples and the rounding
+    // entries of a matrix do not pass its spectral norm; 2 % for the rounding on the way
     plan->sx[t] = pow2_scale(1.02 * top);
-    plan->sa[t] = pow2_scale(1.02 * top * top);
+    plan->sa[t] = pow2_scale(1.02 * end);
     plan->sb[t] = pow2_scale(1.02 * bb);
     top = 1.02 * x;
     if (!(top < 1e6) || !(bb < 1e12)) return false;
@@ -1058,7 +1131,8 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
   {
     TraceScope t("ns_norm", s);
     cudaError_t e = launch_k(ns_norm_kernel, dim3((unsigned)d.chunks, (unsigned)p.batch),
-                             dim3(kNormThreads), 0, s, x, in_f32, (long long)d.elems, d.chunks,
+                             dim3(kNormThreads), 0, s, x, in_f32, d.elems % (in_f32 ? 4 : 8) == 0 ? 1 : 0,
+                             (long long)d.elems, d.chunks,
                              w.partial, w.counts, (int)p.batch + 1);
     if (e != cudaSuccess) return e;
   }
@@ -1066,12 +1140,16 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
     Prep q;
     q.x = x; q.f32 = in_f32; q.form = (int)p.form; q.tall = d.tall; q.chunks = d.chunks;
     q.batch = (int)p.batch; q.tiles_c = (int)(d.ld / 64);
+    q.tiles = (int)(d.R / 64 * (d.ld / 64));
+    q.vec = !skew && !d.tall && p.n * (in_f32 ? 4 : 2) % 16 == 0;
     q.m = p.m; q.n = p.n;
     q.r = (int)d.r; q.k = (int)d.k; q.R = (int)d.R; q.ld = (int)d.ld;
     q.eps = p.eps; q.sx = plan.sx[0]; q.norm_mult = skew ? 2.0 : 1.0;
     q.partial = w.partial; q.out = w.x[0];
+    // few blocks per matrix when there are many, each summing the norm's partials once
+    const int64_t blocks = std::min<int64_t>(q.tiles, std::max<int64_t>(8, 148 * 8 / p.batch));
     TraceScope t("ns_prep", s);
-    cudaError_t e = launch_k(ns_prep_kernel, dim3((unsigned)(d.R / 64 * (d.ld / 64)), (unsigned)p.batch),
+    cudaError_t e = launch_k(ns_prep_kernel, dim3((unsigned)blocks, (unsigned)p.batch),
                              dim3(256), 0, s, q);
     if (e != cudaSuccess) return e;
   }

@@ -9,6 +9,7 @@ library is missing the import fails.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -526,14 +527,19 @@ def layer_norm_bwd(x: torch.Tensor, dy: torch.Tensor, gamma: Optional[torch.Tens
 MUON_COEFFS = (3.4445, -4.7750, 2.0315)
 
 
+@functools.lru_cache(maxsize=64)
+def _coeff_row(a: float, b: float, c: float, steps: int):
+    return (ctypes.c_float * (3 * steps))(*((a, b, c) * steps))
+
+
 def _coeff_array(coeffs, steps: int):
     """[steps][3] floats from one (a, b, c) or from one per step."""
-    rows = [tuple(coeffs)] * steps if len(coeffs) == 3 and not hasattr(coeffs[0], "__len__") \
-        else [tuple(c) for c in coeffs]
+    if len(coeffs) == 3 and not hasattr(coeffs[0], "__len__"):
+        return _coeff_row(*coeffs, max(steps, 0))
+    rows = [tuple(c) for c in coeffs]
     if len(rows) != steps or any(len(r) != 3 for r in rows):
         raise ValueError("coeffs must be one (a, b, c) or one per step")
-    flat = [float(v) for r in rows for v in r]
-    return (ctypes.c_float * len(flat))(*flat)
+    return (ctypes.c_float * (3 * steps))(*(float(v) for r in rows for v in r))
 
 
 def _matrices(x: torch.Tensor):
