@@ -35,9 +35,16 @@ __device__ __forceinline__ float ld_w(const void* w, int w_bf16, int64_t i, floa
                 : static_cast<const float*>(w)[i];
 }
 
-// a variance that rounding left below zero counts as zero (NaN stays NaN)
-__device__ __forceinline__ float rstd_of(float var, float eps) {
-  return 1.f / sqrtf((var < 0.f ? 0.f : var) + eps);
+// rstd of a row from the deviations from its first mean: sq = sum d^2 / m, dm = sum d / m. A
+// variance that rounding left below zero counts as zero (NaN stays NaN). A dm of less than half an
+// ulp of the deviations is dropped: values of few bits and one exponent all round alike when the
+// first mean is subtracted, which looks like a dm of that size, while the first mean of such
+// values is often exact.
+__device__ __forceinline__ float rstd_of(float sq, float& dm, float eps) {
+  float var = sq - dm * dm;
+  var = var < 0.f ? 0.f : var;
+  if (fabsf(dm) <= 0x1p-24f * sqrtf(var)) dm = 0.f;
+  return 1.f / sqrtf(var + eps);
 }
 
 constexpr int kThreads = 256;
@@ -74,8 +81,8 @@ __global__ void __launch_bounds__(kThreads) ln_fwd_any_kernel(const Fwd a) {
       s1 += d;
       s2 += d * d;
     }
-    const float dm = block_sum(s1) / (float)a.m;
-    const float rstd = rstd_of(block_sum(s2) / (float)a.m - dm * dm, a.eps);
+    float dm = block_sum(s1) / (float)a.m;
+    const float rstd = rstd_of(block_sum(s2) / (float)a.m, dm, a.eps);
     for (int64_t i = threadIdx.x; i < a.m; i += kThreads)
       st(y, base + i, (ld(x, base + i) - mean - dm) * rstd * ld_w(a.gamma, a.w_bf16, i, 1.f) +
                           ld_w(a.beta, a.w_bf16, i, 0.f));
@@ -248,6 +255,19 @@ __device__ __forceinline__ void ldw(const WT* p, int i, float none, float (&f)[V
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
+// Sums of a few pairs as a tree: the chains of additions, and with them the rounding, stay short.
+template <int P>
+__device__ __forceinline__ float2 tree(const float2 (&f)[P]) {
+  if constexpr (P == 2) return __fadd2_rn(f[0], f[1]);
+  else return __fadd2_rn(__fadd2_rn(f[0], f[1]), __fadd2_rn(f[2], f[3]));
+}
+template <int P>
+__device__ __forceinline__ float2 tree_of_squares(const float2 (&f)[P]) {
+  const float2 a = __ffma2_rn(f[1], f[1], __fmul2_rn(f[0], f[0]));
+  if constexpr (P == 2) return a;
+  else return __fadd2_rn(a, __ffma2_rn(f[3], f[3], __fmul2_rn(f[2], f[2])));
+}
+
 // Forward: W warps hold R rows, E elements of each per lane, packed as they came; blockDim.y such
 // sets per block. A row is read once and stays in registers over its two sums. What bounds it is
 // instructions as much as bytes, so what a row costs apart from its elements is kept small: W is
@@ -256,8 +276,8 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 // its weights: fp32 gamma and beta of one bf16 row are four times the row's own traffic to L1, which
 // bounded one row per warp (55 us, L1 78 % busy).
 template <typename T, typename WT, int V, int E, int W, int R>
-__global__ void __launch_bounds__(W > 4 ? 32 * W : 128) ln_fwd_kernel(const Fwd a) {
-  constexpr int NV = E / V, Y = W > 4 ? 1 : 4 / W, STEP = 32 * W * V, P = V > 1 ? V / 2 : 1;
+__global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 1 : 4) ln_fwd_kernel(const Fwd a) {
+  constexpr int NV = E / V, Y = W > 4 ? 1 : 4 / W, STEP = 32 * W * V, P = V / 2;
   __shared__ float2 buf[2][Y][R][W];
   pdl_wait();
   pdl_trigger();
@@ -274,12 +294,11 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) ln_fwd_kernel(const Fwd 
       if (j < rows && c0 + STEP * i < m) v[j][i].load(x + j * (int64_t)m + STEP * i);
   const float inv_m = 1.f / (float)m;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // a vector in pairs (a single element: the second of its pair is zero)
   auto pairs = [](const Vec<T, V>& u, float2 (&f)[P]) {
     float e[V];
     u.get(e);
 #pragma unroll
-    for (int k = 0; k < P; ++k) f[k] = make_float2(e[2 * k], V > 1 ? e[(2 * k + 1) % V] : 0.f);
+    for (int k = 0; k < P; ++k) f[k] = make_float2(e[2 * k], e[2 * k + 1]);
   };
   // sums of p over the W warps, per row
   auto reduce = [&](float2 (&p)[R], float2 (*b)[W]) {
@@ -312,8 +331,7 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) ln_fwd_kernel(const Fwd 
     for (int i = 0; i < NV; ++i) {
       if (j < rows && c0 + STEP * i < m) {
         pairs(v[j][i], f);
-#pragma unroll
-        for (int k = 0; k < P; ++k) s = __fadd2_rn(s, f[k]);
+        s = __fadd2_rn(s, tree(f));
       }
     }
     p[j] = make_float2(s.x + s.y, 0.f);
@@ -323,17 +341,14 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) ln_fwd_kernel(const Fwd 
   for (int j = 0; j < R; ++j) {
     mean[j] = p[j].x * inv_m;
     float2 s1 = both(0.f), s2 = both(0.f);
-    const float2 minus = make_float2(-mean[j], V > 1 ? -mean[j] : 0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (j < rows && c0 + STEP * i < m) {
         pairs(v[j][i], f);
 #pragma unroll
-        for (int k = 0; k < P; ++k) {
-          const float2 d = __fadd2_rn(f[k], minus);
-          s1 = __fadd2_rn(s1, d);
-          s2 = __ffma2_rn(d, d, s2);
-        }
+        for (int k = 0; k < P; ++k) f[k] = __fadd2_rn(f[k], both(-mean[j]));
+        s1 = __fadd2_rn(s1, tree(f));
+        s2 = __fadd2_rn(s2, tree_of_squares(f));
       }
     }
     p[j] = make_float2(s1.x + s1.y, s2.x + s2.y);
@@ -342,7 +357,7 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) ln_fwd_kernel(const Fwd 
 #pragma unroll
   for (int j = 0; j < R; ++j) {   // p: dm and rstd
     p[j].x *= inv_m;
-    p[j].y = rstd_of(p[j].y * inv_m - p[j].x * p[j].x, a.eps);
+    p[j].y = rstd_of(p[j].y * inv_m, p[j].x, a.eps);
     if (threadIdx.x == 0 && j < rows) {
       if (a.mean) a.mean[r0 + j] = mean[j] + p[j].x;
       if (a.rstd) a.rstd[r0 + j] = p[j].y;
@@ -366,17 +381,99 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) ln_fwd_kernel(const Fwd 
           pairs(v[j][i], f);
 #pragma unroll
           for (int k = 0; k < P; ++k) {
-            const float2 g2 = make_float2(g[2 * k], g[(2 * k + 1) % V]);
-            const float2 b2 = make_float2(b[2 * k], b[(2 * k + 1) % V]);
+            const float2 g2 = make_float2(g[2 * k], g[2 * k + 1]);
+            const float2 b2 = make_float2(b[2 * k], b[2 * k + 1]);
             const float2 d = __fadd2_rn(__fadd2_rn(f[k], both(-mean[j])), both(-p[j].x));
             const float2 o = __ffma2_rn(__fmul2_rn(d, both(p[j].y)), g2, b2);
             e[2 * k] = o.x;
-            if constexpr (V > 1) e[2 * k + 1] = o.y;
+            e[2 * k + 1] = o.y;
           }
           stv<T, V>(y + j * (int64_t)m + STEP * i, e);
         }
       }
     }
+  }
+}
+
+// The same for rows that do not start on 16 bytes: single elements, held as fp32 pairs (columns
+// c and c + 32 W of a lane), one row at a time.
+template <typename T, typename WT, int E, int W>
+__global__ void __launch_bounds__(W > 4 ? 32 * W : 128) ln_fwd_odd_kernel(const Fwd a) {
+  constexpr int P = E / 2, Y = W > 4 ? 1 : 4 / W, STEP = 32 * W;
+  __shared__ float2 buf[2][Y][W];
+  pdl_wait();
+  pdl_trigger();
+  const int64_t r = (int64_t)blockIdx.x * Y + threadIdx.y;
+  const int m = r < a.T ? (int)a.m : 0;   // a row past the last one has no elements
+  const int c0 = threadIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const T* x = static_cast<const T*>(a.x) + r * a.m + c0;
+  float2 f[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int c = c0 + 2 * STEP * i;
+    f[i].x = c < m ? ld(x, 2 * STEP * i) : 0.f;
+    f[i].y = c + STEP < m ? ld(x, 2 * STEP * i + STEP) : 0.f;
+  }
+  auto reduce = [&](float2 v, float2* b) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    }
+    if constexpr (W > 1) {
+      if (lane == 0) b[warp] = v;
+      __syncthreads();
+      v = both(0.f);
+#pragma unroll
+      for (int w = 0; w < W; ++w) v = __fadd2_rn(v, b[w]);
+    }
+    return v;
+  };
+  const float inv_m = 1.f / (float)a.m;
+  float2 s = both(0.f);
+#pragma unroll
+  for (int i = 0; i < P; i += 4) {
+    const float2 q[4] = {f[i], f[i + 1], f[i + 2], f[i + 3]};
+    s = __fadd2_rn(s, tree(q));
+  }
+  const float mean = reduce(make_float2(s.x + s.y, 0.f), buf[0][threadIdx.y]).x * inv_m;
+  float2 s1 = both(0.f), s2 = both(0.f);
+#pragma unroll
+  for (int i = 0; i < P; i += 4) {
+    float2 q[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = c0 + 2 * STEP * (i + k);
+      q[k] = __fadd2_rn(f[i + k], both(-mean));
+      if (c >= m) q[k].x = 0.f;
+      if (c + STEP >= m) q[k].y = 0.f;
+      f[i + k] = q[k];
+    }
+    s1 = __fadd2_rn(s1, tree(q));
+    s2 = __fadd2_rn(s2, tree_of_squares(q));
+  }
+  const float2 d = reduce(make_float2(s1.x + s1.y, s2.x + s2.y), buf[1][threadIdx.y]);
+  float dm = d.x * inv_m;
+  const float rstd = rstd_of(d.y * inv_m, dm, a.eps);
+  T* y = static_cast<T*>(a.y) + r * a.m + c0;
+  const WT* gamma = static_cast<const WT*>(a.gamma);
+  const WT* beta = static_cast<const WT*>(a.beta);
+  if (gamma) gamma += c0;
+  if (beta) beta += c0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = 2 * STEP * i + STEP * k;
+      if (c0 + c < m) {
+        const float g = gamma ? ld(gamma, c) : 1.f, b = beta ? ld(beta, c) : 0.f;
+        st(y, c, ((k ? f[i].y : f[i].x) - dm) * rstd * g + b);
+      }
+    }
+  }
+  if (threadIdx.x == 0 && m) {
+    if (a.mean) a.mean[r] = mean + dm;
+    if (a.rstd) a.rstd[r] = rstd;
   }
 }
 
@@ -389,14 +486,13 @@ cudaError_t launch_fwd(const Fwd& a, cudaStream_t s) {
                   dim3((unsigned)((a.T + Y * R - 1) / (Y * R))), dim3(32 * W, Y), 0, s, a);
 }
 // E x R values per lane. With rows enough to fill the GPU that way, as many as 64 registers hold
-// (128 of bf16, 64 of fp32, or 64 single elements, which take a register each): rows of 32
-// elements up to 4096 columns and longer pieces of fewer rows beyond, so that a block stays at 128
-// threads (fp32: 256); the barriers of 512 threads cost more than shared weights save (2048 x 16384
-// bf16: 45 us against 35 us). With few rows, one row and 32 elements, or 8 where a warp then
-// holds the row.
+// (128 of bf16, 64 of fp32): rows of 32 elements up to 4096 columns and longer pieces of fewer rows
+// beyond, so that a block stays at 128 threads (fp32: 256); the barriers of 512 threads cost more
+// than shared weights save (2048 x 16384 bf16: 45 us against 35 us). With few rows, one row and
+// 32 elements, or 8 where a warp then holds the row.
 template <typename T, typename WT, int V>
 cudaError_t fwd_width(const Fwd& a, cudaStream_t s) {
-  constexpr int kHold = V == 1 ? 64 : 256 / (int)sizeof(T), kRows = kHold / 32;
+  constexpr int kHold = 256 / (int)sizeof(T), kRows = kHold / 32;
   const bool many = a.T * a.m >= (int64_t)kHold * 32 * 16 * 148;   // 16 warps on every SM
   if (a.m <= 256)
     return many ? launch_fwd<T, WT, V, 8, 1, kRows>(a, s) : launch_fwd<T, WT, V, 8, 1, 1>(a, s);
@@ -407,7 +503,7 @@ cudaError_t fwd_width(const Fwd& a, cudaStream_t s) {
     if constexpr (kHold == 128) {
       if (a.m <= 8192) return launch_fwd<T, WT, V, 64, 4, 2>(a, s);
       return launch_fwd<T, WT, V, 128, 4, 1>(a, s);
-    } else if constexpr (V > 1) {
+    } else {
       if (a.m <= 8192) return launch_fwd<T, WT, V, 64, 4, 1>(a, s);
       return launch_fwd<T, WT, V, 64, 8, 1>(a, s);
     }
@@ -417,6 +513,21 @@ cudaError_t fwd_width(const Fwd& a, cudaStream_t s) {
   if (a.m <= 4096) return launch_fwd<T, WT, V, 32, 4, 1>(a, s);
   if (a.m <= 8192) return launch_fwd<T, WT, V, 32, 8, 1>(a, s);
   return launch_fwd<T, WT, V, 32, 16, 1>(a, s);
+}
+template <typename T, typename WT, int E, int W>
+cudaError_t launch_odd(const Fwd& a, cudaStream_t s) {
+  constexpr int Y = W > 4 ? 1 : 4 / W;
+  return launch_k(ln_fwd_odd_kernel<T, WT, E, W>, dim3((unsigned)((a.T + Y - 1) / Y)),
+                  dim3(32 * W, Y), 0, s, a);
+}
+template <typename T, typename WT>
+cudaError_t fwd_odd(const Fwd& a, cudaStream_t s) {
+  if (a.m <= 256) return launch_odd<T, WT, 8, 1>(a, s);
+  if (a.m <= 1024) return launch_odd<T, WT, 32, 1>(a, s);
+  if (a.m <= 2048) return launch_odd<T, WT, 32, 2>(a, s);
+  if (a.m <= 4096) return launch_odd<T, WT, 32, 4>(a, s);
+  if (a.m <= 8192) return launch_odd<T, WT, 32, 8>(a, s);
+  return launch_odd<T, WT, 32, 16>(a, s);
 }
 
 // ------------------------------------------------------------------ rows through a ring
@@ -630,8 +741,14 @@ __global__ void __launch_bounds__(1024, 1) ln_bwd_ring_kernel(const Bwd a, const
             const float h = (x[0] - mean[j]) * rstd[j], gk = d[0] * w[0];
             ag[i] += d[0] * h;
             ab[i] += d[0];
-            s1.x += gk;
-            s2.x += gk * h;
+            // (two chains of sums each)
+            if (i & 1) {
+              s1.y += gk;
+              s2.y += gk * h;
+            } else {
+              s1.x += gk;
+              s2.x += gk * h;
+            }
           } else {
 #pragma unroll
             for (int k = 0; k < P; ++k) {
@@ -807,10 +924,10 @@ cudaError_t fwd(const Fwd& a, DT t, cudaStream_t s) {
     const bool vec = a.m * (t == DT::BF16 ? 2 : 4) % 16 == 0;   // every row starts on 16 bytes
     if (t == DT::BF16) {
       if (vec) return a.w_bf16 ? fwd_width<bf16, bf16, 8>(a, s) : fwd_width<bf16, float, 8>(a, s);
-      return a.w_bf16 ? fwd_width<bf16, bf16, 1>(a, s) : fwd_width<bf16, float, 1>(a, s);
+      return a.w_bf16 ? fwd_odd<bf16, bf16>(a, s) : fwd_odd<bf16, float>(a, s);
     }
     if (vec) return a.w_bf16 ? fwd_width<float, bf16, 4>(a, s) : fwd_width<float, float, 4>(a, s);
-    return a.w_bf16 ? fwd_width<float, bf16, 1>(a, s) : fwd_width<float, float, 1>(a, s);
+    return a.w_bf16 ? fwd_odd<float, bf16>(a, s) : fwd_odd<float, float>(a, s);
   }
   const dim3 grid((unsigned)row_blocks(a.T)), block(kThreads);
   return t == DT::BF16 ? launch_k(ln_fwd_any_kernel<bf16>, grid, block, 0, s, a)
