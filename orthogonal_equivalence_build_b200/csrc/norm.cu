@@ -634,11 +634,14 @@ struct Ring {
     return reinterpret_cast<const T*>(smem + (size_t)(s * ARR + k) * sh.slot +
                                       ((g * rows * row_bytes) & 15) + r * row_bytes);
   }
-  // After the barrier of the current group: the slot of the group before it has been read by every
-  // thread and takes the next group to come; on to the next slot.
+  // After the barrier of the current group, on to the next slot. Its own slot (LATER: the slot of
+  // the group before, when the current one is read once more behind the barrier) has been read by
+  // every thread and takes the next group to come.
+  template <bool LATER>
   __device__ __forceinline__ void release() {
-    if (used++ > 0) {
-      if (tid() == 0 && next < groups) fetch(next, s == 0 ? sh.stages - 1 : s - 1);
+    if (!LATER || used++ > 0) {
+      if (tid() == 0 && next < groups)
+        fetch(next, !LATER ? s : s == 0 ? sh.stages - 1 : s - 1);
       next += gridDim.x;
     }
     if (++s == sh.stages) { s = 0; ph ^= 1u; }
@@ -656,19 +659,19 @@ struct Ring {
 
 // Backward. A thread has the same E columns in every row (vector i starts at column
 // (i blockDim.x + threadIdx.x) V), so its shares of dgamma and dbeta stay in registers to the end,
-// are added over the block's rows in shared memory and written once per block; E = 8 keeps its
-// gammas too. A group is R rows for each of blockDim.y sets of threads. Per group there is one barrier:
-// it completes the row sums, and it frees the slot of the group before, which was read for
-// the last time since the previous barrier; x and dy are read from their slot twice rather than
-// kept in registers.
-template <typename T, typename WT, int V, int E, int R>
-__global__ void __launch_bounds__(1024, 1) ln_bwd_ring_kernel(const Bwd a, const RingShape shape) {
+// are added over the block's rows in shared memory and written once per block. A group is R rows
+// for each of blockDim.y sets of threads; per group there is one barrier, which completes the row
+// sums and frees a slot. E = 8 keeps gamma in registers. KEEP also keeps xh and g of the R rows over
+// the barrier (16 registers a row: 16384 x 4096 bf16 96 -> 89 us); otherwise x and dy are read from
+// their slot a second time (8192 x 5120 bf16, 640 threads: 64 us against 71 us kept).
+template <typename T, typename WT, int V, int E, int R, int MAXT, bool KEEP>
+__global__ void __launch_bounds__(MAXT, 1) ln_bwd_ring_kernel(const Bwd a, const RingShape shape) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kMaxStages];
-  __shared__ float2 buf[2][32 * R];
+  __shared__ float buf[2][MAXT / 32 * R * 2];     // [set][row][s1 of its warps, s2 of its warps]
   __shared__ int abort_flag;
-  constexpr int NV = E / V, P = V > 1 ? V / 2 : 1;
-  constexpr bool KEEP = E == 8;
+  constexpr int NV = E / V, P = E / 2;
+  constexpr bool KEEP_W = E == 8;
   const int m = (int)a.m, warps = blockDim.x >> 5, step = blockDim.x * V;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Ring<T, V, 2> ring;
@@ -680,24 +683,54 @@ __global__ void __launch_bounds__(1024, 1) ln_bwd_ring_kernel(const Bwd a, const
   ring.start();
   const WT* gamma = static_cast<const WT*>(a.gamma);
   const int c0 = threadIdx.x * V;
-  float gm[KEEP ? NV : 1][V];
-  if constexpr (KEEP) {
+  // this thread's E values of a row in pairs; columns past the width read as `none`
+  auto row_pairs = [&](const T* p, int live, float none, float2 (&f)[P]) {
+    float* e = reinterpret_cast<float*>(f);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (c0 + i * step < m) ldw<WT, V>(gamma, c0 + i * step, 1.f, gm[i]);
-  }
-  float ag[E], ab[E];
+    for (int i = 0; i < NV; ++i) {
+      float v[V];
 #pragma unroll
-  for (int k = 0; k < E; ++k) ag[k] = ab[k] = 0.f;
+      for (int k = 0; k < V; ++k) v[k] = none;
+      if (c0 + i * step < live) {
+        Vec<T, V> w;
+        w.load(p + i * step);
+        w.get(v);
+      }
+#pragma unroll
+      for (int k = 0; k < V; ++k) e[i * V + k] = v[k];
+    }
+  };
+  auto weights = [&](auto& f) {
+    float* e = reinterpret_cast<float*>(f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float v[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[k] = 0.f;
+      if (c0 + i * step < m) ldw<WT, V>(gamma, c0 + i * step, 1.f, v);
+#pragma unroll
+      for (int k = 0; k < V; ++k) e[i * V + k] = v[k];
+    }
+  };
+  float2 gm[KEEP_W ? P : 1], ag[P], ab[P];
+  if constexpr (KEEP_W) weights(gm);
+  auto weight = [&](int i, float (&w)[V]) {   // of vector i
+    if constexpr (KEEP_W) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) w[k] = reinterpret_cast<const float*>(gm)[i * V + k];
+    } else {
+      ldw<WT, V>(gamma, c0 + i * step, 1.f, w);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < P; ++k) ag[k] = ab[k] = both(0.f);
   float mean_n[R], rstd_n[R];                // of the next group's rows
   auto stats = [&](int64_t g) {
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       const int64_t r = g * ring.rows + threadIdx.y * R + j;
-      if (r < a.T) {
-        mean_n[j] = __ldg(a.mean + r);
-        rstd_n[j] = __ldg(a.rstd + r);
-      }
+      mean_n[j] = r < a.T ? __ldg(a.mean + r) : 0.f;
+      rstd_n[j] = r < a.T ? __ldg(a.rstd + r) : 0.f;
     }
   };
   stats(blockIdx.x);
@@ -716,52 +749,66 @@ __global__ void __launch_bounds__(1024, 1) ln_bwd_ring_kernel(const Bwd a, const
     const bool ok = ring.wait(g);
     const T* px = ring.row(g, 0, threadIdx.y * R) + c0;
     const T* pd = ring.row(g, 1, threadIdx.y * R) + c0;
-    float2* sums = buf[turn] + threadIdx.y * R * warps;   // (the other one may still be read)
+    float* sums = buf[turn] + threadIdx.y * R * 2 * warps;   // (the other one may still be read)
     turn ^= 1;
+    float2 xh[KEEP ? R : 1][KEEP ? P : 1], gd[KEEP ? R : 1][KEEP ? P : 1];
 #pragma unroll
     for (int j = 0; j < R; ++j) {
+      const int live = j < rows ? m : 0;
       float2 s1 = both(0.f), s2 = both(0.f);
+      if constexpr (KEEP) {
+        // past the width or the last row: x = mean and dy = 0, which add nothing
+        float2(&h)[P] = xh[j];
+        float2(&d)[P] = gd[j];
+        row_pairs(px + j * m, live, mean[j], h);
+        row_pairs(pd + j * m, live, 0.f, d);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = c0 + i * step;
-        if (j < rows && c < m) {
-          Vec<T, V> vx, vd;
-          float x[V], d[V], w[V];
-          vx.load(px + j * m + i * step);
-          vd.load(pd + j * m + i * step);
-          vx.get(x);
-          vd.get(d);
-          if constexpr (KEEP) {
+        for (int k = 0; k < P; ++k) {
+          h[k] = __fmul2_rn(__fadd2_rn(h[k], both(-mean[j])), both(rstd[j]));
+          ag[k] = __ffma2_rn(d[k], h[k], ag[k]);
+          ab[k] = __fadd2_rn(ab[k], d[k]);
+          d[k] = __fmul2_rn(d[k], gm[k]);
+          s1 = __fadd2_rn(s1, d[k]);
+          s2 = __ffma2_rn(d[k], h[k], s2);
+        }
+      } else {
+        float* eg = reinterpret_cast<float*>(ag);
+        float* eb = reinterpret_cast<float*>(ab);
 #pragma unroll
-            for (int k = 0; k < V; ++k) w[k] = gm[i][k];
-          } else {
-            ldw<WT, V>(gamma, c, 1.f, w);
-          }
-          if constexpr (V == 1) {
-            const float h = (x[0] - mean[j]) * rstd[j], gk = d[0] * w[0];
-            ag[i] += d[0] * h;
-            ab[i] += d[0];
-            // (two chains of sums each)
-            if (i & 1) {
-              s1.y += gk;
-              s2.y += gk * h;
+        for (int i = 0; i < NV; ++i) {
+          const int c = c0 + i * step;
+          if (c < live) {
+            Vec<T, V> vx, vd;
+            float x[V], d[V], w[V];
+            vx.load(px + j * m + i * step);
+            vd.load(pd + j * m + i * step);
+            vx.get(x);
+            vd.get(d);
+            weight(i, w);
+            if constexpr (V == 1) {
+              const float h = (x[0] - mean[j]) * rstd[j], gk = d[0] * w[0];
+              eg[i] += d[0] * h;
+              eb[i] += d[0];
+              if (i & 1) {   // (two chains of sums each)
+                s1.y += gk;
+                s2.y += gk * h;
+              } else {
+                s1.x += gk;
+                s2.x += gk * h;
+              }
             } else {
-              s1.x += gk;
-              s2.x += gk * h;
-            }
-          } else {
 #pragma unroll
-            for (int k = 0; k < P; ++k) {
-              const float2 d2 = make_float2(d[2 * k], d[2 * k + 1]);
-              const float2 h = __fmul2_rn(
-                  __fadd2_rn(make_float2(x[2 * k], x[2 * k + 1]), both(-mean[j])), both(rstd[j]));
-              const float2 gk = __fmul2_rn(d2, make_float2(w[2 * k], w[2 * k + 1]));
-              float2* eg = reinterpret_cast<float2*>(ag + i * V) + k;
-              float2* eb = reinterpret_cast<float2*>(ab + i * V) + k;
-              *eg = __ffma2_rn(d2, h, *eg);
-              *eb = __fadd2_rn(*eb, d2);
-              s1 = __fadd2_rn(s1, gk);
-              s2 = __ffma2_rn(gk, h, s2);
+              for (int k = 0; k < V / 2; ++k) {
+                const int q = i * V / 2 + k;
+                const float2 d2 = make_float2(d[2 * k], d[2 * k + 1]);
+                const float2 h = __fmul2_rn(
+                    __fadd2_rn(make_float2(x[2 * k], x[2 * k + 1]), both(-mean[j])), both(rstd[j]));
+                const float2 gk = __fmul2_rn(d2, make_float2(w[2 * k], w[2 * k + 1]));
+                ag[q] = __ffma2_rn(d2, h, ag[q]);
+                ab[q] = __fadd2_rn(ab[q], d2);
+                s1 = __fadd2_rn(s1, gk);
+                s2 = __ffma2_rn(gk, h, s2);
+              }
             }
           }
         }
@@ -772,56 +819,75 @@ __global__ void __launch_bounds__(1024, 1) ln_bwd_ring_kernel(const Bwd a, const
       t += __shfl_xor_sync(0xffffffffu, (lane & 16) ? t1 : t2, 16);
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      if ((lane & 15) == 0) reinterpret_cast<float*>(sums + j * warps + warp)[lane >> 4] = t;
+      if ((lane & 15) == 0) sums[j * 2 * warps + (lane >> 4) * warps + warp] = t;
     }
     if (g + gridDim.x < ring.groups) stats(g + gridDim.x);
     bad = __syncthreads_or(!ok);
     if (bad) break;
-    ring.release();
+    ring.template release<!KEEP>();
     if (a.dx) {
       T* dx = static_cast<T*>(a.dx) + r0 * a.m + c0;
 #pragma unroll
       for (int j = 0; j < R; ++j) {
-        // the row's sums over its warps, by the warp's lanes
-        float2 t = lane < warps ? sums[j * warps + lane] : both(0.f);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
-          t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
+        const int live = j < rows ? m : 0;
+        // the row's sums over its warps: the lower half-warp s1, the upper one s2
+        const float* mine = sums + j * 2 * warps + (lane >> 4) * warps;
+        const int w = lane & 15;
+        const float lo = mine[min(w, warps - 1)];
+        float t = w < warps ? lo : 0.f;
+        if constexpr (MAXT > 512) {
+          const float hi = mine[min(w + 16, warps - 1)];
+          t += w + 16 < warps ? hi : 0.f;
         }
-        const float c1 = t.x * inv_m, c2 = t.y * inv_m;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int c = c0 + i * step;
-          if (j < rows && c < m) {
-            Vec<T, V> vx, vd;
-            float x[V], d[V], w[V];
-            vx.load(px + j * m + i * step);
-            vd.load(pd + j * m + i * step);
-            vx.get(x);
-            vd.get(d);
-            if constexpr (KEEP) {
+        for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        const float c1 = __shfl_sync(0xffffffffu, t, 0) * inv_m;
+        const float c2 = __shfl_sync(0xffffffffu, t, 16) * inv_m;
+        // rstd (g - c1 - xh c2)
+        if constexpr (KEEP) {
+          float2(&h)[P] = xh[j];
+          float2(&d)[P] = gd[j];
+          const float* e = reinterpret_cast<const float*>(d);
 #pragma unroll
-              for (int k = 0; k < V; ++k) w[k] = gm[i][k];
-            } else {
-              ldw<WT, V>(gamma, c, 1.f, w);
-            }
-            // rstd (g - c1 - xh c2)
-            if constexpr (V == 1) {
-              d[0] = rstd[j] * (d[0] * w[0] - c1 - (x[0] - mean[j]) * rstd[j] * c2);
-            } else {
+          for (int k = 0; k < P; ++k)
+            d[k] = __fmul2_rn(__ffma2_rn(h[k], both(-c2), __fadd2_rn(d[k], both(-c1))),
+                              both(rstd[j]));
 #pragma unroll
-              for (int k = 0; k < P; ++k) {
-                const float2 h = __fmul2_rn(
-                    __fadd2_rn(make_float2(x[2 * k], x[2 * k + 1]), both(-mean[j])), both(rstd[j]));
-                float2 e = __ffma2_rn(make_float2(d[2 * k], d[2 * k + 1]),
-                                      make_float2(w[2 * k], w[2 * k + 1]), both(-c1));
-                e = __fmul2_rn(__ffma2_rn(h, both(-c2), e), both(rstd[j]));
-                d[2 * k] = e.x;
-                d[2 * k + 1] = e.y;
+          for (int i = 0; i < NV; ++i) {
+            float v[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) v[k] = e[i * V + k];
+            if (c0 + i * step < live) stv<T, V>(dx + j * (int64_t)m + i * step, v);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            const int c = c0 + i * step;
+            if (c < live) {
+              Vec<T, V> vx, vd;
+              float x[V], d[V], w[V];
+              vx.load(px + j * m + i * step);
+              vd.load(pd + j * m + i * step);
+              vx.get(x);
+              vd.get(d);
+              weight(i, w);
+              if constexpr (V == 1) {
+                d[0] = rstd[j] * (d[0] * w[0] - c1 - (x[0] - mean[j]) * rstd[j] * c2);
+              } else {
+#pragma unroll
+                for (int k = 0; k < V / 2; ++k) {
+                  const float2 h = __fmul2_rn(
+                      __fadd2_rn(make_float2(x[2 * k], x[2 * k + 1]), both(-mean[j])),
+                      both(rstd[j]));
+                  float2 e = __ffma2_rn(make_float2(d[2 * k], d[2 * k + 1]),
+                                        make_float2(w[2 * k], w[2 * k + 1]), both(-c1));
+                  e = __fmul2_rn(__ffma2_rn(h, both(-c2), e), both(rstd[j]));
+                  d[2 * k] = e.x;
+                  d[2 * k + 1] = e.y;
+                }
               }
+              stv<T, V>(dx + j * (int64_t)m + i * step, d);
             }
-            stv<T, V>(dx + j * (int64_t)m + i * step, d);
           }
         }
       }
@@ -835,6 +901,8 @@ __global__ void __launch_bounds__(1024, 1) ln_bwd_ring_kernel(const Bwd a, const
   // the block's column sums, its sets of threads added in order; no copy is in flight any more
   float* out_g = a.part + (int64_t)blockIdx.x * m;
   float* out_b = a.part + ((int64_t)gridDim.x + blockIdx.x) * m;
+  const float* eg = reinterpret_cast<const float*>(ag);
+  const float* eb = reinterpret_cast<const float*>(ab);
   float* sh = reinterpret_cast<float*>(smem);    // [sets][2][m]
   __syncthreads();
 #pragma unroll
@@ -843,8 +911,8 @@ __global__ void __launch_bounds__(1024, 1) ln_bwd_ring_kernel(const Bwd a, const
     if (c < m) {
 #pragma unroll
       for (int k = 0; k < V; ++k) {
-        sh[(threadIdx.y * 2) * m + c + k] = ag[i * V + k];
-        sh[(threadIdx.y * 2 + 1) * m + c + k] = ab[i * V + k];
+        sh[(threadIdx.y * 2) * m + c + k] = eg[i * V + k];
+        sh[(threadIdx.y * 2 + 1) * m + c + k] = eb[i * V + k];
       }
     }
   }
@@ -863,24 +931,26 @@ __global__ void __launch_bounds__(1024, 1) ln_bwd_ring_kernel(const Bwd a, const
 constexpr int kMaxParts = 148;   // one block per SM
 
 // Shape of the one-pass backward for a width; stages < 2: a row is too wide for the ring. E = 8 up to
-// 8192 columns (a row then has at most 1024 threads), 16 beyond; `sets` sets of threads and R rows
-// each (two share their addresses and the barrier; one where single elements use up the registers)
-// make a group, at most 64 KB of x and dy (three slots in flight) and no more than leaves
-// a group for every SM.
+// 8192 columns (a row then has at most 1024 threads), 32 beyond. `sets` sets of threads and R rows
+// each make a group: at most 64 KB of x and dy (three slots in flight), no more than leaves a group
+// for every SM; R up to 4 in blocks of 512 threads, 2 in larger ones.
 struct GroupShape {
   int threads, sets, E, R;
   RingShape ring;
   size_t smem;
 };
-GroupShape group_shape(int64_t T, int64_t m, int esz, bool vec) {
+GroupShape group_shape(int64_t T, int64_t m, int esz) {
   GroupShape sh;
-  sh.E = m <= 8192 ? 8 : 16;
+  sh.E = m <= 8192 ? 8 : 32;
   sh.threads = 32 * (int)((m + 32 * sh.E - 1) / (32 * sh.E));
+  const int most = sh.E == 32 ? 1 : sh.threads > 512 ? 2 : 4;
   const int64_t fit = 64 * 1024 / (2 * m * esz);                  // rows in 64 KB
   const int64_t share = (T + kMaxParts - 1) / kMaxParts;          // rows per SM
   const int64_t rows = std::max<int64_t>(1, std::min(fit, share));
-  sh.R = sh.E == 8 && vec && rows >= 2 ? 2 : 1;
-  sh.sets = (int)std::max<int64_t>(1, std::min<int64_t>(1024 / sh.threads, rows / sh.R));
+  sh.R = most;
+  while (sh.R > rows) sh.R /= 2;
+  const int block = most == 4 ? 512 : sh.threads;
+  sh.sets = (int)std::max<int64_t>(1, std::min<int64_t>(block / sh.threads, rows / sh.R));
   // the window around unaligned rows needs up to 30 bytes more
   sh.ring.slot = (int)(((int64_t)sh.sets * sh.R * m * esz + 31) / 16 * 16);
   const int64_t stage = 2 * (int64_t)sh.ring.slot;
@@ -890,9 +960,9 @@ GroupShape group_shape(int64_t T, int64_t m, int esz, bool vec) {
   return sh;
 }
 
-template <typename T, typename WT, int V, int E, int R>
+template <typename T, typename WT, int V, int E, int R, int MAXT, bool KEEP>
 cudaError_t launch_bwd_er(const Bwd& a, const GroupShape& sh, cudaStream_t s) {
-  auto kern = ln_bwd_ring_kernel<T, WT, V, E, R>;
+  auto kern = ln_bwd_ring_kernel<T, WT, V, E, R, MAXT, KEEP>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem);
   if (e != cudaSuccess) return e;
@@ -901,10 +971,14 @@ cudaError_t launch_bwd_er(const Bwd& a, const GroupShape& sh, cudaStream_t s) {
 }
 template <typename T, typename WT, int V>
 cudaError_t launch_bwd(const Bwd& a, const GroupShape& sh, cudaStream_t s) {
-  if (sh.E == 16) return launch_bwd_er<T, WT, V, 16, 1>(a, sh, s);
-  if constexpr (V > 1)
-    if (sh.R == 2) return launch_bwd_er<T, WT, V, 8, 2>(a, sh, s);
-  return launch_bwd_er<T, WT, V, 8, 1>(a, sh, s);
+  if (sh.E == 32) return launch_bwd_er<T, WT, V, 32, 1, 512, false>(a, sh, s);
+  if (sh.threads <= 512) {
+    if (sh.R == 4) return launch_bwd_er<T, WT, V, 8, 4, 512, true>(a, sh, s);
+    if (sh.R == 2) return launch_bwd_er<T, WT, V, 8, 2, 512, true>(a, sh, s);
+    return launch_bwd_er<T, WT, V, 8, 1, 512, true>(a, sh, s);
+  }
+  return sh.R == 2 ? launch_bwd_er<T, WT, V, 8, 2, 1024, false>(a, sh, s)
+                   : launch_bwd_er<T, WT, V, 8, 1, 1024, true>(a, sh, s);
 }
 
 int row_blocks(int64_t T) { return (int)std::min<int64_t>(T, 148 * 8); }
@@ -944,7 +1018,7 @@ cudaError_t bwd(Bwd a, DT t, void* ws, cudaStream_t s) {
   if (!a.err) return cudaErrorUnknown;
   cudaError_t e = cudaSuccess;
   const bool vec = a.m * esz % 16 == 0;   // every row starts on 16 bytes
-  const GroupShape sh = a.m <= kRegWidth ? group_shape(a.T, a.m, esz, vec) : GroupShape{};
+  const GroupShape sh = a.m <= kRegWidth ? group_shape(a.T, a.m, esz) : GroupShape{};
   if (a.m <= kRegWidth && sh.ring.stages >= 2) {
     const int64_t groups = (a.T + sh.sets * sh.R - 1) / (sh.sets * sh.R);
     a.parts = (int)std::min<int64_t>(groups, kMaxParts);
