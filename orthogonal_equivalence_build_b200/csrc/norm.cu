@@ -531,9 +531,10 @@ cudaError_t fwd_odd(const Fwd& a, cudaStream_t s) {
 }
 
 // ------------------------------------------------------------------ rows through a ring
-// A persistent block takes groups of consecutive rows. They come through a ring of shared-memory slots by bulk copies, groups ahead, so that bytes are
-// in flight whatever the block waits for. Elements are worked on in pairs (fp32 x 2
-// instructions): at bf16's two bytes an element, instructions count as much as bytes.
+// A persistent block takes groups of consecutive rows. They come through a ring of shared-memory
+// slots by bulk copies, groups ahead, so that bytes are in flight whatever the block waits for.
+// Elements are worked on in pairs (fp32 x 2 instructions): at bf16's two bytes an element,
+// instructions count as much as bytes.
 // Rows that do not start on 16 bytes (V = 1) are copied as the 16-byte window around them.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar) {
@@ -544,7 +545,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-constexpr int kRingBytes = 192 * 1024;   // per SM
+constexpr int kRingBytes = 224 * 1024;   // of the 227 KB of a block
 constexpr int kMaxStages = 6;
 
 struct RingShape {
@@ -663,7 +664,9 @@ struct Ring {
 // for each of blockDim.y sets of threads; per group there is one barrier, which completes the row
 // sums and frees a slot. E = 8 keeps gamma in registers. KEEP also keeps xh and g of the R rows over
 // the barrier (16 registers a row: 16384 x 4096 bf16 96 -> 89 us); otherwise x and dy are read from
-// their slot a second time (8192 x 5120 bf16, 640 threads: 64 us against 71 us kept).
+// their slot a second time (8192 x 5120 bf16, 640 threads: 66 us against 71 us kept). What is left
+// above the bytes' time is each group's chain, sums - barrier - sums of the warps - dx; two halves of
+// a block working one group apart did not hide it (97 us at 16384 x 4096: groups of half the rows).
 template <typename T, typename WT, int V, int E, int R, int MAXT, bool KEEP>
 __global__ void __launch_bounds__(MAXT, 1) ln_bwd_ring_kernel(const Bwd a, const RingShape shape) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -833,11 +836,12 @@ __global__ void __launch_bounds__(MAXT, 1) ln_bwd_ring_kernel(const Bwd a, const
         // the row's sums over its warps: the lower half-warp s1, the upper one s2
         const float* mine = sums + j * 2 * warps + (lane >> 4) * warps;
         const int w = lane & 15;
-        const float lo = mine[min(w, warps - 1)];
-        float t = w < warps ? lo : 0.f;
-        if constexpr (MAXT > 512) {
-          const float hi = mine[min(w + 16, warps - 1)];
-          t += w + 16 < warps ? hi : 0.f;
+        float t;
+        if constexpr (MAXT <= 512) {
+          t = w < warps ? mine[w] : 0.f;
+        } else {   // (loads without a branch: 4096 x 8192 fp32 70 us against 92 us)
+          const float lo = mine[min(w, warps - 1)], hi = mine[min(w + 16, warps - 1)];
+          t = (w < warps ? lo : 0.f) + (w + 16 < warps ? hi : 0.f);
         }
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);

@@ -4,8 +4,8 @@
 Tolerances, element by element, with u = 2^-24 and `adds` the longest chain of fp32 additions that
 a row sum can take (a warp per row at least: m / 32 + 32): a sum is off by at most adds u of the sum
 of its magnitudes. x - mean is off by e_x = 4 u (|x - first mean| + spread of the mean's error)
-after the correction of the first mean; rstd, products and the final scaling add a few u each. Outputs
-round once: 2^-9 of the value for half a bf16 step taken as 2^-8, or 2^-24.
+after the correction of the first mean; rstd, products and the final scaling add a few u each.
+Outputs round once: half a step is 2^-8 (bf16) or 2^-24 (fp32) of the value.
 """
 import ctypes
 
@@ -130,6 +130,20 @@ SHAPES = [(1, 1), (3, 1), (1, 2), (2, 3), (1, 7), (5, 8), (1, 64), (300, 31), (3
 @pytest.mark.parametrize("T,m", SHAPES)
 def test_forward_and_backward(T, m, dt, wt):
     x, dy, gamma, beta = make(T, m, dt, wt)
+    y, mean, rstd = run_fwd(x, gamma, beta)
+    check_fwd(x, gamma, beta, y, mean, rstd, dt, 1e-5)
+    dx, dg, db = run_bwd(x, dy, gamma, mean, rstd)
+    check_bwd(x, dy, gamma, mean, rstd, dx, dg, db, dt)
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("m", [200, 1016, 2040, 4088, 8184, 13312, 16384])
+def test_rows_that_fill_the_gpu(m, dt):
+    """Enough elements (9.7M of bf16, 4.9M of fp32) for several rows per warp or set of threads; the
+    last group of rows is not full."""
+    T = (9_800_000 if dt == "bf16" else 4_900_000) // m | 1
+    x, dy, gamma, beta = make(T, m, dt, "f32")
     y, mean, rstd = run_fwd(x, gamma, beta)
     check_fwd(x, gamma, beta, y, mean, rstd, dt, 1e-5)
     dx, dg, db = run_bwd(x, dy, gamma, mean, rstd)
