@@ -313,7 +313,8 @@ poetx_status poetx_dequantize_w0(const int8_t* wq, const float* scale, int64_t m
  *   (3.4445, -4.7750, 2.0315) every singular value above ~1e-3 of the norm comes out near 1 in
  *   five steps; (1.875, -1.25, 0.375) converges to 1 exactly, in more steps.
  *   x [batch, m, n] (x_dtype, F32 or BF16), read only. out [batch, m, n] (out_dtype, F32 or
- *   BF16); out may be x. m > n is worked on from the other side (same result).
+ *   BF16); out may be x if their types agree. m > n is worked on from the other side (same
+ *   result).
  *   coeffs: HOST array [steps][3] of (a_t, b_t, c_t), read before the call returns; steps in
  *   1..POETX_ORTH_MAX_STEPS. eps >= 0: 0 / 0 for a matrix of zeros with eps = 0 gives NaN, as the
  *   formula does; with eps > 0 zeros give zeros. The norm is summed in 64 bits. A matrix that
@@ -322,7 +323,7 @@ poetx_status poetx_dequantize_w0(const int8_t* wq, const float* scale, int64_t m
  *   of the iteration; BF16 outputs to about one more bf16 rounding (operands are fp16 parts).
  *   Deterministic: the same inputs give the same bits.
  *   workspace >= poetx_orthogonalize_workspace_bytes(batch, m, n, steps) (0 for sizes that the call
- *   refuses or that need no work).
+ *   refuses or that need none: both sides at most 128); one workspace serves one call at a time.
  *   Errors: INVALID_ARG (NULL, negative size, steps, eps, scale, coefficients that are not finite
  *   or under which a singular value of [0, 1] passes 1e6), SHAPE (m or n > 65536, batch > 65535),
  *   DTYPE, ALIGN, WORKSPACE, CUDA.

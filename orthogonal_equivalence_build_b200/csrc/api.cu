@@ -975,6 +975,8 @@ poetx_status check_orth(const char* what, orth::Problem* p, int64_t batch, int64
 poetx_status run_orth(const char* what, const orth::Problem& p, const orth::Plan& plan,
                       const void* x, void* out, void* workspace, size_t ws_bytes, void* stream) {
   if (!x || !out) return fail(POETX_ERR_INVALID_ARG, "%s: a pointer is NULL", what);
+  if (x == out && p.in_t != p.out_t)
+    return fail(POETX_ERR_INVALID_ARG, "%s: in place with two dtypes", what);
   if (!aligned16(x) || !aligned16(out))
     return fail(POETX_ERR_ALIGN, "%s: pointers must be 16-byte aligned", what);
   poetx_status st = check_ws(workspace, ws_bytes, orth::workspace_bytes(p));

@@ -61,20 +61,17 @@ constexpr int kEpiStage = 2 * kPiece;      // per epilogue warp
 constexpr int kSlots = 8;
 
 // ------------------------------------------------------------------ the work
-// Tile shapes. CG = 1: 128 x 128 tiles of one CTA; CG = 2: 256 x TN tiles of a CTA pair
+// Tile shapes. CG = 1: 128 x 128 tiles of one CTA; CG = 2: 256 x 256 tiles of a CTA pair
 // (cta_group::2: each CTA holds 128 rows of A, half of B's columns and 128 rows of the result).
-template <int CG_, int TN_>
+template <int CG_>
 struct Shape {
-  static constexpr int CG = CG_, TM = 128 * CG_, TN = TN_;
-  static constexpr int BN = TN / CG;                    // columns of B that a CTA loads
-  static constexpr int A_BYTES = 128 * BK * 2, B_BYTES = BN * BK * 2;
-  // (three 32 KB stages are enough while X fits L2, and cost 15 % where it does not)
-  static constexpr int STAGES = A_BYTES + B_BYTES > 24576 ? 5 : 6;
-  static constexpr int COLS = TN / 2;                   // result columns of an epilogue warp
-  static constexpr size_t SMEM =
-      (size_t)STAGES * (A_BYTES + B_BYTES) + kEpiWarps * kEpiStage + 1024 + 512;
+  static constexpr int CG = CG_, TILE = 128 * CG_;
+  static constexpr int COLS = TILE / 2;                 // result columns of an epilogue warp
 };
-
+constexpr int kOperand = 128 * BK * 2;     // bytes of a CTA's rows of A, and of its columns of B
+// (three stages are enough while X fits L2, and cost 15 % where it does not)
+constexpr int STAGES = 5;
+constexpr size_t kSmem = (size_t)STAGES * 2 * kOperand + kEpiWarps * kEpiStage + 1024 + 512;
 
 struct Kind {
   int tiles_m, tiles_n, per;   // tile grid of a matrix; tiles computed
@@ -84,7 +81,7 @@ struct Job {
   Kind k[3];
   int batch, steps, per_step, total;   // tiles per step (all matrices) and in all
   int R;                               // padded rows of every result
-  int exact, skew;
+  int exact;
   int fmode, out_f32, vec;             // the caller's array: layout, type, rows start on 16 bytes
   void* out;
   long long um, un;                    // its rows and columns (of the result as computed)
@@ -93,10 +90,10 @@ struct Job {
   float fa[kMaxSteps], da[kMaxSteps];  // square: + fa A + da I
 };
 struct Maps {
-  CUtensorMap xa[2], xb[2], xn[2];   // X: left operand, right operand K- and N-major,
-  CUtensorMap xs[2], xm[2];          //    pieces as computed and mirrored
-  CUtensorMap aa, ab, as, am;        // A: left and right operand, pieces
-  CUtensorMap ba, bs, bm;            // B: left operand, pieces
+  CUtensorMap xk[2], xn[2];   // X: operand read K-major, right operand read N-major,
+  CUtensorMap xs[2], xm[2];   //    pieces as computed and mirrored
+  CUtensorMap ak, as, am;     // A: operand, pieces
+  CUtensorMap bk, bs, bm;     // B: operand, pieces
 };
 
 struct Work {
@@ -106,7 +103,6 @@ struct Work {
 // Tile numbers count through step, product, matrix, tile. Symmetric results: row by row over the
 // tiles on and above the diagonal. Others: bands of 16 row tiles sweep the columns, so a band
 // of the left operand stays in L2 while X streams.
-template <typename S>
 __device__ __forceinline__ Work decode(const Job& j, int tile) {
   Work w;
   w.t = tile / j.per_step;
@@ -118,11 +114,10 @@ __device__ __forceinline__ Work decode(const Job& j, int tile) {
   w.g = l / k.per;
   l -= w.g * k.per;
   if (k.sym) {
-    constexpr int Q = S::TM / S::TN;
     int i = 0;
-    while (l >= k.tiles_n - Q * i) l -= k.tiles_n - Q * i++;
+    while (l >= k.tiles_n - i) l -= k.tiles_n - i++;
     w.mb = i;
-    w.nb = Q * i + l;
+    w.nb = i + l;
   } else {
     const int band = l / (16 * k.tiles_n), first = band * 16;
     const int gm = min(16, k.tiles_m - first), r = l - band * 16 * k.tiles_n;
@@ -168,10 +163,10 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, 
       : "memory");
 }
 
-// kind::f16, fp16 operands, fp32 accumulator, TM x TN tile; bit 16: B is N-major
+// kind::f16, fp16 operands, fp32 accumulator, TILE x TILE; bit 16: B is N-major
 template <typename S>
 __device__ __forceinline__ constexpr uint32_t idesc() {
-  return (1u << 4) | ((uint32_t)(S::TN >> 3) << 17) | ((uint32_t)(S::TM >> 4) << 24);
+  return (1u << 4) | ((uint32_t)(S::TILE >> 3) << 17) | ((uint32_t)(S::TILE >> 4) << 24);
 }
 
 // until *cnt >= target
@@ -366,14 +361,14 @@ __device__ __forceinline__ void emit_user(const Job& p, const float* v, float f,
 template <typename S>
 __global__ void __launch_bounds__(kThreads, 1)
 ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
-  constexpr int CG = S::CG, TN = S::TN, STAGES = S::STAGES;
-  constexpr uint32_t TMEM_COLS = 2 * TN;
+  constexpr int CG = S::CG, TILE = S::TILE;
+  constexpr uint32_t TMEM_COLS = 2 * TILE;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sa = smem;
-  uint8_t* sb = smem + STAGES * S::A_BYTES;
-  uint8_t* sepi = sb + STAGES * S::B_BYTES;
+  uint8_t* sb = smem + STAGES * kOperand;
+  uint8_t* sepi = sb + STAGES * kOperand;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sepi + kEpiWarps * kEpiStage);
   uint64_t* full = bars;                     // [STAGES], leader only
   uint64_t* empty = full + STAGES;           // [STAGES]
@@ -488,7 +483,7 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
           break;
         }
         if (tile >= job.total) break;
-        const Work w = decode<S>(job, tile);
+        const Work w = decode(job, tile);
         const Kind& k = job.k[w.kind];
         const int before = w.t * (job.k[0].per + job.k[1].per + job.k[2].per) +
                            (w.kind > 0 ? job.k[0].per : 0) + (w.kind > 1 ? job.k[1].per : 0);
@@ -503,10 +498,10 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
         if (elect_one()) mbar_arrive(smem_u32(wready + n % kSlots));
         const int x = w.t & 1;
         const CUtensorMap* ma =
-            w.kind == kGram ? &maps.xa[x] : w.kind == kSquare ? &maps.aa : &maps.ba;
+            w.kind == kGram ? &maps.xk[x] : w.kind == kSquare ? &maps.ak : &maps.bk;
         const CUtensorMap* mb =
-            w.kind == kGram ? &maps.xb[x] : w.kind == kSquare ? &maps.ab : &maps.xn[x];
-        const int am = w.mb * S::TM + (int)rank * 128, bn = w.nb * TN + (int)rank * S::BN;
+            w.kind == kGram ? &maps.xk[x] : w.kind == kSquare ? &maps.ak : &maps.xn[x];
+        const int am = w.mb * TILE + (int)rank * 128, bn = w.nb * TILE + (int)rank * 128;
         const int ns = segments(job, w);
         for (int seg = 0; ok && seg < ns; ++seg) {
           const int za = part_a(ns, seg) * job.batch + w.g, zb = part_b(ns, seg) * job.batch + w.g;
@@ -517,14 +512,14 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
                              /*stop_on_abort=*/false);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             const uint32_t fb = fb0 + (uint32_t)(s * 8);
-            const uint32_t da = smem_u32(sa) + (uint32_t)(s * S::A_BYTES);
-            const uint32_t db = smem_u32(sb) + (uint32_t)(s * S::B_BYTES);
+            const uint32_t da = smem_u32(sa) + (uint32_t)(s * kOperand);
+            const uint32_t db = smem_u32(sb) + (uint32_t)(s * kOperand);
             if (elect_one()) {
-              if (leader) mbar_expect_tx(smem_u32(full + s), CG * (S::A_BYTES + S::B_BYTES));
+              if (leader) mbar_expect_tx(smem_u32(full + s), CG * 2 * kOperand);
               load_box<CG>(da, ma, fb, kk, am, za);
               if (w.kind == kUpdate) {
                 load_box<CG>(db, mb, fb, bn, kk, zb);
-                if constexpr (S::BN == 128) load_box<CG>(db + 64 * BK * 2, mb, fb, bn + 64, kk, zb);
+                load_box<CG>(db + 64 * BK * 2, mb, fb, bn + 64, kk, zb);
               } else {
                 load_box<CG>(db, mb, fb, kk, bn, zb);
               }
@@ -553,7 +548,7 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
         for (int n = 0; ok; ++n) {
           int tile;
           if (!(ok = take(n, tile)) || tile >= job.total) break;
-          const Work w = decode<S>(job, tile);
+          const Work w = decode(job, tile);
           const int ns = segments(job, w), nk1 = job.k[w.kind].nk, nk = ns * nk1;
           const bool mn = w.kind == kUpdate;
           const uint32_t id = idesc<S>() | (mn ? 1u << 16 : 0u);
@@ -565,13 +560,13 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
             ok = wait_inline(smem_u32(tempty + acc), ((uint32_t)(count >> 1) & 1u) ^ 1u, ctl, kErrMma);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after();
-            const uint32_t d = tmem_base + (uint32_t)(acc * TN);
+            const uint32_t d = tmem_base + (uint32_t)(acc * TILE);
             for (uint32_t more = 0u; kb < end; ++kb, more = 1u) {
               ok = wait_inline(smem_u32(full + s), ph, ctl, kErrMma);
               if (!(ok = __all_sync(0xffffffffu, ok))) break;
               tc_fence_after();
-              const uint32_t a = a_lo + (uint32_t)s * (S::A_BYTES >> 4);
-              const uint32_t b = b_lo + (uint32_t)s * (S::B_BYTES >> 4);
+              const uint32_t a = a_lo + (uint32_t)s * (kOperand >> 4);
+              const uint32_t b = b_lo + (uint32_t)s * (kOperand >> 4);
               if (elect_one()) {
                 mma<CG>(d, a, b, id, more);
 #pragma unroll
@@ -605,11 +600,11 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
     for (int n = 0; ok; ++n) {
       int tile;
       if (!take(n, tile) || tile >= job.total) break;
-      const Work w = decode<S>(job, tile);
+      const Work w = decode(job, tile);
       const Kind& k = job.k[w.kind];
       const int ns = segments(job, w), nk = ns * k.nk, head = head_blocks(job, ns, k.nk);
-      const int row0 = w.mb * S::TM + (int)rank * 128 + quarter * 32;
-      const int base0 = w.nb * TN + cbase;
+      const int row0 = w.mb * TILE + (int)rank * 128 + quarter * 32;
+      const int base0 = w.nb * TILE + cbase;
       // A's 64 columns from c on, for b A, into the stage (which the warp has finished with)
       auto load_a = [&](int c) {
         if (lane == 0) {
@@ -638,7 +633,7 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
         const uint32_t trow = tmem_base + ((uint32_t)(quarter * 32) << 16) +
-                              (uint32_t)(acc * TN + cbase);
+                              (uint32_t)(acc * TILE + cbase);
 #pragma unroll
         for (int c = 0; c < COLS; c += 32) {
           uint32_t r[32];
@@ -701,7 +696,7 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
           w.kind == kGram ? &maps.as : w.kind == kSquare ? &maps.bs : &maps.xs[x];
       const CUtensorMap* to_mirror =
           w.kind == kGram ? &maps.am : w.kind == kSquare ? &maps.bm : &maps.xm[x];
-      const bool mirror = k.sym && w.nb >= (w.mb + 1) * (S::TM / TN);
+      const bool mirror = k.sym && w.nb > w.mb;
       // bf16 results: the last update reads one part of X
       const int parts = job.exact || (w.kind == kUpdate && w.t + 2 < job.steps) ? 2 : 1;
 #pragma unroll
@@ -966,55 +961,53 @@ int sm_total() {
   return n > 0 ? n : 148;
 }
 
-Kind kind_of(int64_t rows, int64_t cols, int64_t K, int tm, int tn, bool sym) {
+Kind kind_of(int64_t rows, int64_t cols, int64_t K, int tile, bool sym) {
   Kind k;
-  k.tiles_m = (int)((rows + tm - 1) / tm);
-  k.tiles_n = (int)((cols + tn - 1) / tn);
+  k.tiles_m = (int)((rows + tile - 1) / tile);
+  k.tiles_n = (int)((cols + tile - 1) / tile);
   k.sym = sym;
   k.cols = (int)cols;
   k.nk = (int)(K / BK);
-  k.per = k.tiles_m * k.tiles_n;
-  if (sym) {
-    k.per = 0;
-    for (int i = 0; i < k.tiles_m; ++i) k.per += k.tiles_n - tm / tn * i;
-  }
+  k.per = sym ? k.tiles_n * (k.tiles_n + 1) / 2 : k.tiles_m * k.tiles_n;   // (sym: square)
   return k;
 }
 
-// Tile shape and use of symmetry of a problem.
+// Tile shape (CTAs that share a tile) and use of symmetry of a problem.
 struct Choice {
-  int cg, tn;
+  int cg;
   bool sym;
 };
-// The fastest of them by a model of one step: the work of all matrices shared out over the GPU, and
+// The fastest of three by a model of one step: the work of all matrices shared out over the GPU, and
 // one matrix's three products one after the other, each in whole waves of tiles; the longer of the
-// two and a quarter of the other. Rates as measured (us): a 64-deep K block of a 256 x 256, 256 x
-// 128 (CTA pair) or 128 x 128 tile (one CTA) 0.31, 0.26, 0.26 in a chain, 0.33, 0.35, 0.33 with
-// every SM busy (small tiles are then bound by L2); 64 columns of an epilogue warp on their way
-// out 1 per part, 2.2 if mirrored; 3 from a product's last store to the next one's first load.
-// Measured against the other choices (in one run each): 8B up bf16 256 x 256 symmetric 4.4 ms,
-// full 5.5, 256 x 128 5.6; 36 blocks of 512 128 x 128 symmetric 398 us, 256 x 256 425, 256 x 128 467;
-// 3 of 1000 x 333 256 x 128 full 229, symmetric 248, 256 x 256 383; 4096 x 1024 bf16 263 against 311.
+// two and a third of the other. Its figures (us) are a fit to 54 problems of 1 to 100 matrices of
+// 192 to 4096 rows: the choice takes at most 6 % more than the best of the three. Where symmetry or
+// the large tile pays, and where it does not (256 x 256 symmetric, 128 x 128 symmetric, 128 x 128
+// full, us in one run): 4096 x 4096 bf16 1643, 2138, 2687; 36 blocks of 512 499, 464, 668;
+// 4096 x 1024 bf16 314, 265, 259; 3 of 1000 x 333 fp32 282, 214, 199. Never the fastest, and so not
+// here: 256 x 256 full (2113, 534, 305, 282); 256 x 128 tiles of a pair (at most 3 % ahead of
+// 128 x 128: 4096 x 1024 fp32 544, 551).
 Choice choose(const Problem& p, const Dims& d, int sms) {
   const bool exact = p.out_t == DT::F32, skew = p.form == Form::Skew;
-  if (d.R <= 128) return {1, 128, false};   // one row of tiles: nothing to mirror
-  Choice best{2, 256, true};
+  if (d.R <= 128) return {1, false};   // one row of tiles: nothing to mirror
+  Choice best{};
   double best_t = 1e30;
-  for (const Choice c : {Choice{2, 256, true}, Choice{2, 128, true}, Choice{2, 256, false},
-                         Choice{2, 128, false}, Choice{1, 128, true}, Choice{1, 128, false}}) {
-    const int tm = 128 * c.cg, workers = sms / c.cg;
-    const double busy_us = c.tn == 256 || c.cg == 1 ? 0.33 : 0.35;
-    const double block_us = c.tn == 256 ? 0.31 : 0.26;
+  for (const Choice c : {Choice{2, true}, Choice{1, true}, Choice{1, false}}) {
+    const int tile = 128 * c.cg, workers = sms / c.cg;
+    // a K block with every SM busy and in a chain; a tile's way out per part, and what a product
+    // takes besides from its last store to the next one's first load
+    const double busy_us = c.cg == 2 ? 0.47 : 0.33, block_us = c.cg == 2 ? 0.28 : 0.17;
+    const double part_us = c.cg == 2 ? 3.6 : 2.6, gap_us = c.cg == 2 ? 4.0 : 2.2;
     double work = 0.0, chain = 0.0;
     for (int kind = 0; kind < 3; ++kind) {
       const bool sym = c.sym && (kind < 2 || skew);
-      const Kind k = kind_of(d.R, kind < 2 ? d.R : d.ld, kind == 0 ? d.ld : d.R, tm, c.tn, sym);
+      const Kind k = kind_of(d.R, kind < 2 ? d.R : d.ld, kind == 0 ? d.ld : d.R, tile, sym);
       const int blocks = k.nk * (exact ? 3 : kind == 2 ? 2 : 1);
-      const double out = c.tn / 128 * (exact || kind == 2 ? 2 : 1) * (sym ? 2.2 : 1.0);
+      const double out =
+          part_us * (exact || kind == 2 ? 2 : 1) * (sym && k.per > 1 ? 1.25 : 1.0);
       work += (double)p.batch * k.per * std::max(blocks * busy_us, out) / workers;
-      chain += std::ceil((double)k.per / workers) * blocks * block_us + out + 3.0;
+      chain += std::ceil((double)k.per / workers) * blocks * block_us + out + gap_us;
     }
-    const double t = std::max(work, chain) + 0.25 * std::min(work, chain);
+    const double t = std::max(work, chain) + std::min(work, chain) / 3.0;
     if (t < best_t) { best_t = t; best = c; }
   }
   return best;
@@ -1023,7 +1016,7 @@ Choice choose(const Problem& p, const Dims& d, int sms) {
 template <typename S>
 cudaError_t launch(const Maps& maps, const Job& job, int sms, cudaStream_t s) {
   auto kern = ns_kernel<S>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
   // setmaxnreg waits for registers that the block was not launched with: refuse such a build
   static const int regs = [kern] {
@@ -1043,7 +1036,7 @@ cudaError_t launch(const Maps& maps, const Job& job, int sms, cudaStream_t s) {
   for (const Kind& k : job.k) most = std::max(most, k.per * job.batch);
   cfg.gridDim = dim3((unsigned)(S::CG * std::min(most, sms / S::CG)));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = S::SMEM;
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = S::CG == 2 ? 2 : 1;
@@ -1115,7 +1108,9 @@ void fill_factors(const Problem& p, const Plan& plan, float (*f)[kMaxSteps], flo
   }
 }
 
-size_t workspace_bytes(const Problem& p) { return layout(p, nullptr, nullptr); }
+size_t workspace_bytes(const Problem& p) {
+  return small_fits(p) ? 0 : layout(p, nullptr, nullptr);
+}
 
 cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, void* ws,
                 cudaStream_t s) {
@@ -1155,7 +1150,7 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
   }
   const int sms = sm_total();
   const Choice c = choose(p, d, sms);
-  const int tm = 128 * c.cg, bn = c.tn / c.cg;
+  const int tile = 128 * c.cg;
 
   Maps maps{};
   const int64_t mats = 2 * p.batch;
@@ -1163,25 +1158,23 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
   bool ok = true;
   for (int i = 0; i < 2; ++i) {
     if (!w.x[i]) continue;
-    ok = ok && make_map3(&maps.xa[i], w.x[i], mats, d.R, d.ld, 64, 128, k128) &&
-         make_map3(&maps.xb[i], w.x[i], mats, d.R, d.ld, 64, bn, k128) &&
+    ok = ok && make_map3(&maps.xk[i], w.x[i], mats, d.R, d.ld, 64, 128, k128) &&
          make_map3(&maps.xn[i], w.x[i], mats, d.R, d.ld, 64, 64, k128) &&
          make_map3(&maps.xs[i], w.x[i], mats, d.R, d.ld, 64, 32, k128) &&
          make_map3(&maps.xm[i], w.x[i], mats, d.R, d.ld, 32, 64, k64);
   }
-  ok = ok && make_map3(&maps.aa, w.a, mats, d.R, d.R, 64, 128, k128) &&
-       make_map3(&maps.ab, w.a, mats, d.R, d.R, 64, bn, k128) &&
+  ok = ok && make_map3(&maps.ak, w.a, mats, d.R, d.R, 64, 128, k128) &&
        make_map3(&maps.as, w.a, mats, d.R, d.R, 64, 32, k128) &&
        make_map3(&maps.am, w.a, mats, d.R, d.R, 32, 64, k64) &&
-       make_map3(&maps.ba, w.b, mats, d.R, d.R, 64, 128, k128) &&
+       make_map3(&maps.bk, w.b, mats, d.R, d.R, 64, 128, k128) &&
        make_map3(&maps.bs, w.b, mats, d.R, d.R, 64, 32, k128) &&
        make_map3(&maps.bm, w.b, mats, d.R, d.R, 32, 64, k64);
   if (!ok) return cudaErrorInvalidValue;
 
   Job job{};
-  job.k[kGram] = kind_of(d.R, d.R, d.ld, tm, c.tn, c.sym);
-  job.k[kSquare] = kind_of(d.R, d.R, d.R, tm, c.tn, c.sym);
-  job.k[kUpdate] = kind_of(d.R, d.ld, d.R, tm, c.tn, c.sym && skew);
+  job.k[kGram] = kind_of(d.R, d.R, d.ld, tile, c.sym);
+  job.k[kSquare] = kind_of(d.R, d.R, d.R, tile, c.sym);
+  job.k[kUpdate] = kind_of(d.R, d.ld, d.R, tile, c.sym && skew);
   job.batch = (int)p.batch;
   job.steps = p.steps;
   int64_t per_step = 0;
@@ -1192,7 +1185,6 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
   job.total = job.per_step * p.steps;
   job.R = (int)d.R;
   job.exact = exact;
-  job.skew = skew;
   job.fmode = skew ? kPacked : d.tall ? kTransposed : kRows;
   job.out = out;
   job.out_f32 = exact;
@@ -1203,9 +1195,7 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
   job.done = w.counts + 1;
   job.err = err;
   fill_factors(p, plan, job.f, job.fa, job.da);
-  if (c.cg == 1) return launch<Shape<1, 128>>(maps, job, sms, s);
-  return c.tn == 256 ? launch<Shape<2, 256>>(maps, job, sms, s)
-                     : launch<Shape<2, 128>>(maps, job, sms, s);
+  return c.cg == 1 ? launch<Shape<1>>(maps, job, sms, s) : launch<Shape<2>>(maps, job, sms, s);
 }
 
 }  // namespace orth

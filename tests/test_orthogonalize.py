@@ -45,6 +45,7 @@ def newton_schulz64(x, coeffs, eps, scale=1.0):
 
 def bound(its, coeffs, out_bf16, scale):
     err = 0.0
+    s = np.linalg.svd(its[0], compute_uv=False)   # of X_t; the next ones are |p(s)|
     for t, (a, b, c) in enumerate(coeffs):
         X = its[t]
         if X.shape[0] > X.shape[1]:
@@ -59,15 +60,14 @@ def bound(its, coeffs, out_bf16, scale):
         A = X @ X.T
         H = b * np.eye(r) + c * A
         B = a * np.eye(r) + A @ H
-        n2 = lambda m: np.linalg.norm(m, 2)
+        x2, a2, h2 = s.max(), s.max() ** 2, np.abs(b + c * s ** 2).max()   # spectral norms
         nf = np.linalg.norm
         acc = (k / 16 + 16) * 2.0 ** -23 * nf(X) ** 2
         acc_r = (r / 16 + 16) * 2.0 ** -23
-        gram = 2 * u_g * n2(X) * nf(X) + acc
+        gram = 2 * u_g * x2 * nf(X) + acc
         dA = u_m * nf(A) + gram
         dH = u_m * nf(H) + abs(c) * gram
-        dB = u_m * nf(B) + n2(H) * dA + n2(A) * dH + acc_r * nf(A) * nf(H)
-        s = np.linalg.svd(X, compute_uv=False)
+        dB = u_m * nf(B) + h2 * dA + a2 * dH + acc_r * nf(A) * nf(H)
         p = a * s + b * s ** 3 + c * s ** 5
         dp = a + 3 * b * s ** 2 + 5 * c * s ** 4
         ds, sm = s[:, None] - s[None, :], s[:, None] + s[None, :]
@@ -75,7 +75,8 @@ def bound(its, coeffs, out_bf16, scale):
         div = np.where(close, dp[:, None], (p[:, None] - p[None, :]) / np.where(close, 1.0, ds))
         gain = max(np.abs(div).max(),
                    np.abs((p[:, None] + p[None, :]) / np.maximum(sm, 1e-30)).max(), abs(a))
-        err = gain * (err + u_x * nf(X)) + n2(X) * dB + acc_r * nf(B) * nf(X)
+        err = gain * (err + u_x * nf(X)) + x2 * dB + acc_r * nf(B) * nf(X)
+        s = np.abs(p)
     X = its[-1]
     return abs(scale) * (err + (2.0 ** -8 if out_bf16 else 2.0 ** -24) * np.linalg.norm(X))
 
@@ -109,7 +110,8 @@ def run(x, coeffs, out_dtype, **kw):
 
 SHAPES = [(1, 1, 1), (1, 1, 7), (2, 5, 3), (1, 64, 64), (3, 65, 130), (2, 130, 65),
           (1, 128, 300), (1, 257, 257), (2, 300, 1000), (1, 1000, 333), (4, 512, 512),
-          (40, 256, 256), (38, 200, 521), (2, 1100, 1300)]
+          (40, 256, 256), (38, 200, 521), (2, 1100, 1300), (12, 700, 640),
+          (2, 1800, 1700), (3, 1500, 1550)]
 
 
 @gpu
@@ -208,8 +210,9 @@ def test_in_place_two_dimensional_and_same_bits():
 
 @gpu
 @pytest.mark.parametrize("xt", ["f32", "bf16"])
-def test_writes_only_its_output_and_workspace(xt):
-    x = torch.randn(3, 70, 41, device="cuda").to(DT[xt])
+@pytest.mark.parametrize("shape", [(3, 70, 41), (3, 170, 141), (3, 1500, 1601)])
+def test_writes_only_its_output_and_workspace(shape, xt):
+    x = torch.randn(*shape, device="cuda").to(DT[xt])
     need = poetx.orthogonalize_workspace_bytes(x, x)
     buf = torch.full((need + 512,), 0x5A, dtype=torch.uint8, device="cuda")
     ws = buf[256:256 + need]
@@ -233,7 +236,8 @@ def unpack(u, b):
 
 @gpu
 @pytest.mark.parametrize("nb,b", [(1, 2), (3, 3), (5, 7), (16, 64), (2, 100), (3, 128), (4, 200),
-                                  (40, 256), (9, 512), (1, 777), (2, 1024)])
+                                  (40, 256), (9, 512), (1, 777), (2, 1024), (12, 777),
+                                  (16, 1000)])
 def test_packed_blocks(nb, b):
     rng = np.random.default_rng(b)
     u = torch.from_numpy(rng.standard_normal((nb, b * (b - 1) // 2)) * 1e-3).float().cuda()
@@ -329,16 +333,16 @@ def _call(x=0x10000, xt=0, batch=1, m=64, n=64, coeffs=MUON, steps=1, eps=1e-7, 
     (dict(m=65537), 2), (dict(n=70000), 2), (dict(batch=65536), 2),
     (dict(batch=65535, m=65536, n=65536), 2),
     (dict(xt=7), 4), (dict(ot=-1), 4), (dict(x=0x10008), 3), (dict(out=0x20004), 3),
-    (dict(), 8), (dict(ws=0x30000, wsb=1024), 8),
+    (dict(m=200), 8), (dict(m=200, ws=0x30000, wsb=1024), 8), (dict(out=0x10000, ot=1), 1),
 ])
 def test_refusals(kw, status):
     assert _call(**kw) == status
 
 
 def test_workspace_alignment_and_empty_calls():
-    need = poetx.lib.poetx_orthogonalize_workspace_bytes(1, 64, 64, 1)
-    assert need > 0
-    assert _call(ws=0x30008, wsb=need) == 3
+    need = poetx.lib.poetx_orthogonalize_workspace_bytes(1, 200, 64, 1)
+    assert need > 0 and poetx.lib.poetx_orthogonalize_workspace_bytes(1, 128, 128, 1) == 0
+    assert _call(m=200, ws=0x30008, wsb=need) == 3
     for kw in (dict(batch=0), dict(m=0), dict(n=0)):
         assert _call(x=None, out=None, **kw) == 0
     assert poetx.lib.poetx_orthogonalize_workspace_bytes(1, 0, 64, 1) == 0
@@ -348,7 +352,7 @@ def test_workspace_alignment_and_empty_calls():
 
 @pytest.mark.parametrize("kw,status", [
     (dict(b=1), 1), (dict(b=1025), 2), (dict(nb=-1), 1), (dict(nb=65536), 2), (dict(u=None), 1),
-    (dict(out=None), 1), (dict(u=0x10004), 3), (dict(steps=0), 1), (dict(), 8), (dict(nb=0), 0),
+    (dict(out=None), 1), (dict(u=0x10004), 3), (dict(steps=0), 1), (dict(b=200), 8), (dict(nb=0), 0),
 ])
 def test_packed_refusals(kw, status):
     a = dict(u=0x10000, nb=2, b=64, steps=1, out=0x20000)
