@@ -191,6 +191,7 @@ template <typename T, int V>
 struct Vec {
   uint4 w;
   __device__ __forceinline__ void load(const T* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void clear() { w = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void get(float (&f)[V]) const {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -208,6 +209,7 @@ template <typename T>
 struct Vec<T, 1> {
   T w;
   __device__ __forceinline__ void load(const T* p) { w = *p; }
+  __device__ __forceinline__ void clear() { st(&w, 0, 0.f); }
   __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = ld(&w, 0); }
 };
 template <typename T, int V>
@@ -562,7 +564,7 @@ struct Ring {
   uint64_t* full;
   umma::Ctl ctl;
   RingShape sh;
-  int64_t row_bytes, total, groups, next;
+  int64_t group_bytes, total, groups, next;
   int rows, s, used;
   uint32_t ph;
 
@@ -570,11 +572,13 @@ struct Ring {
   // bytes of group g: [lo, hi) of the arrays, copied as [from, end)
   __device__ __forceinline__ void window(int64_t g, int64_t& lo, int64_t& hi, int64_t& from,
                                          int64_t& end) const {
-    lo = g * rows * row_bytes;
-    hi = min(total, lo + rows * row_bytes);
-    from = lo & ~(int64_t)15;
-    end = min((hi + 15) & ~(int64_t)15, total & ~(int64_t)15);
-    if (end < from) end = from;
+    lo = from = g * group_bytes;
+    hi = end = min(total, lo + group_bytes);
+    if constexpr (V == 1) {
+      from = lo & ~(int64_t)15;
+      end = min((hi + 15) & ~(int64_t)15, total & ~(int64_t)15);
+      if (end < from) end = from;
+    }
   }
   __device__ __forceinline__ void fetch(int64_t g, int slot) const {
     int64_t lo, hi, from, end;
@@ -592,8 +596,8 @@ struct Ring {
                                        RingShape shape, int64_t T_, int64_t m, int rows_) {
     smem = buf; full = bars; sh = shape; rows = rows_;
     ctl = umma::Ctl{abort_flag, err};
-    row_bytes = m * sizeof(T);
-    total = T_ * row_bytes;
+    group_bytes = rows * m * sizeof(T);
+    total = T_ * m * sizeof(T);
     groups = (T_ + rows - 1) / rows;
     s = used = 0;
     ph = 0;
@@ -630,21 +634,29 @@ struct Ring {
     }
     return ok;
   }
-  // row `r` of the current slot's group
-  __device__ __forceinline__ const T* row(int64_t g, int k, int r) const {
-    return reinterpret_cast<const T*>(smem + (size_t)(s * ARR + k) * sh.slot +
-                                      ((g * rows * row_bytes) & 15) + r * row_bytes);
+  // first row of the current slot's group
+  __device__ __forceinline__ const T* row(int64_t g, int k) const {
+    const T* p = reinterpret_cast<const T*>(smem + (size_t)(s * ARR + k) * sh.slot);
+    if constexpr (V == 1) p += (g * group_bytes & 15) / sizeof(T);
+    return p;
   }
-  // After the barrier of the current group, on to the next slot. Its own slot (LATER: the slot of
-  // the group before, when the current one is read once more behind the barrier) has been read by
-  // every thread and takes the next group to come.
-  template <bool LATER>
+  // After the barrier of the current group, on to the next slot. Its own slot has been read by every
+  // thread and takes the next group to come.
   __device__ __forceinline__ void release() {
-    if (!LATER || used++ > 0) {
-      if (tid() == 0 && next < groups)
-        fetch(next, !LATER ? s : s == 0 ? sh.stages - 1 : s - 1);
-      next += gridDim.x;
-    }
+    refill(s);
+    advance();
+  }
+  // The same where the slot is read once more behind the barrier: what takes the next group is the
+  // slot of the group before.
+  __device__ __forceinline__ void release_before() {
+    if (used++ > 0) refill(s == 0 ? sh.stages - 1 : s - 1);
+    advance();
+  }
+  __device__ __forceinline__ void refill(int slot) {
+    if (tid() == 0 && next < groups) fetch(next, slot);
+    next += gridDim.x;
+  }
+  __device__ __forceinline__ void advance() {
     if (++s == sh.stages) { s = 0; ph ^= 1u; }
   }
   // let the copies in flight land before the block leaves
@@ -658,259 +670,17 @@ struct Ring {
   }
 };
 
-// Backward. A thread has the same E columns in every row (vector i starts at column
-// (i blockDim.x + threadIdx.x) V), so its shares of dgamma and dbeta stay in registers to the end,
-// are added over the block's rows in shared memory and written once per block. A group is R rows
-// for each of blockDim.y sets of threads; per group there is one barrier, which completes the row
-// sums and frees a slot. E = 8 keeps gamma in registers. KEEP also keeps xh and g of the R rows over
-// the barrier (16 registers a row: 16384 x 4096 bf16 96 -> 89 us); otherwise x and dy are read from
-// their slot a second time (8192 x 5120 bf16, 640 threads: 66 us against 71 us kept). What is left
-// above the bytes' time is each group's chain, sums - barrier - sums of the warps - dx; two halves of
-// a block working one group apart did not hide it (97 us at 16384 x 4096: groups of half the rows).
-template <typename T, typename WT, int V, int E, int R, int MAXT, bool KEEP>
-__global__ void __launch_bounds__(MAXT, 1) ln_bwd_ring_kernel(const Bwd a, const RingShape shape) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t full[kMaxStages];
-  __shared__ float buf[2][MAXT / 32 * R * 2];     // [set][row][s1 of its warps, s2 of its warps]
-  __shared__ int abort_flag;
-  constexpr int NV = E / V, P = E / 2;
-  constexpr bool KEEP_W = E == 8;
-  const int m = (int)a.m, warps = blockDim.x >> 5, step = blockDim.x * V;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Ring<T, V, 2> ring;
-  ring.src[0] = static_cast<const char*>(a.x);
-  ring.src[1] = static_cast<const char*>(a.dy);
-  ring.init(smem, full, &abort_flag, a.err, shape, a.T, a.m, blockDim.y * R);
-  pdl_wait();
-  pdl_trigger();
-  ring.start();
-  const WT* gamma = static_cast<const WT*>(a.gamma);
-  const int c0 = threadIdx.x * V;
-  // this thread's E values of a row in pairs; columns past the width read as `none`
-  auto row_pairs = [&](const T* p, int live, float none, float2 (&f)[P]) {
-    float* e = reinterpret_cast<float*>(f);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float v[V];
-#pragma unroll
-      for (int k = 0; k < V; ++k) v[k] = none;
-      if (c0 + i * step < live) {
-        Vec<T, V> w;
-        w.load(p + i * step);
-        w.get(v);
-      }
-#pragma unroll
-      for (int k = 0; k < V; ++k) e[i * V + k] = v[k];
-    }
-  };
-  auto weights = [&](auto& f) {
-    float* e = reinterpret_cast<float*>(f);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float v[V];
-#pragma unroll
-      for (int k = 0; k < V; ++k) v[k] = 0.f;
-      if (c0 + i * step < m) ldw<WT, V>(gamma, c0 + i * step, 1.f, v);
-#pragma unroll
-      for (int k = 0; k < V; ++k) e[i * V + k] = v[k];
-    }
-  };
-  float2 gm[KEEP_W ? P : 1], ag[P], ab[P];
-  if constexpr (KEEP_W) weights(gm);
-  auto weight = [&](int i, float (&w)[V]) {   // of vector i
-    if constexpr (KEEP_W) {
-#pragma unroll
-      for (int k = 0; k < V; ++k) w[k] = reinterpret_cast<const float*>(gm)[i * V + k];
-    } else {
-      ldw<WT, V>(gamma, c0 + i * step, 1.f, w);
-    }
-  };
-#pragma unroll
-  for (int k = 0; k < P; ++k) ag[k] = ab[k] = both(0.f);
-  float mean_n[R], rstd_n[R];                // of the next group's rows
-  auto stats = [&](int64_t g) {
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const int64_t r = g * ring.rows + threadIdx.y * R + j;
-      mean_n[j] = r < a.T ? __ldg(a.mean + r) : 0.f;
-      rstd_n[j] = r < a.T ? __ldg(a.rstd + r) : 0.f;
-    }
-  };
-  stats(blockIdx.x);
-  const float inv_m = 1.f / (float)m;
-  bool bad = false;
-  int turn = 0;
-  for (int64_t g = blockIdx.x; g < ring.groups; g += gridDim.x) {
-    const int64_t r0 = g * ring.rows + threadIdx.y * R;
-    const int rows = (int)max((int64_t)0, min((int64_t)R, a.T - r0));
-    float mean[R], rstd[R];
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      mean[j] = mean_n[j];
-      rstd[j] = rstd_n[j];
-    }
-    const bool ok = ring.wait(g);
-    const T* px = ring.row(g, 0, threadIdx.y * R) + c0;
-    const T* pd = ring.row(g, 1, threadIdx.y * R) + c0;
-    float* sums = buf[turn] + threadIdx.y * R * 2 * warps;   // (the other one may still be read)
-    turn ^= 1;
-    float2 xh[KEEP ? R : 1][KEEP ? P : 1], gd[KEEP ? R : 1][KEEP ? P : 1];
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const int live = j < rows ? m : 0;
-      float2 s1 = both(0.f), s2 = both(0.f);
-      if constexpr (KEEP) {
-        // past the width or the last row: x = mean and dy = 0, which add nothing
-        float2(&h)[P] = xh[j];
-        float2(&d)[P] = gd[j];
-        row_pairs(px + j * m, live, mean[j], h);
-        row_pairs(pd + j * m, live, 0.f, d);
-#pragma unroll
-        for (int k = 0; k < P; ++k) {
-          h[k] = __fmul2_rn(__fadd2_rn(h[k], both(-mean[j])), both(rstd[j]));
-          ag[k] = __ffma2_rn(d[k], h[k], ag[k]);
-          ab[k] = __fadd2_rn(ab[k], d[k]);
-          d[k] = __fmul2_rn(d[k], gm[k]);
-          s1 = __fadd2_rn(s1, d[k]);
-          s2 = __ffma2_rn(d[k], h[k], s2);
-        }
-      } else {
-        float* eg = reinterpret_cast<float*>(ag);
-        float* eb = reinterpret_cast<float*>(ab);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int c = c0 + i * step;
-          if (c < live) {
-            Vec<T, V> vx, vd;
-            float x[V], d[V], w[V];
-            vx.load(px + j * m + i * step);
-            vd.load(pd + j * m + i * step);
-            vx.get(x);
-            vd.get(d);
-            weight(i, w);
-            if constexpr (V == 1) {
-              const float h = (x[0] - mean[j]) * rstd[j], gk = d[0] * w[0];
-              eg[i] += d[0] * h;
-              eb[i] += d[0];
-              if (i & 1) {   // (two chains of sums each)
-                s1.y += gk;
-                s2.y += gk * h;
-              } else {
-                s1.x += gk;
-                s2.x += gk * h;
-              }
-            } else {
-#pragma unroll
-              for (int k = 0; k < V / 2; ++k) {
-                const int q = i * V / 2 + k;
-                const float2 d2 = make_float2(d[2 * k], d[2 * k + 1]);
-                const float2 h = __fmul2_rn(
-                    __fadd2_rn(make_float2(x[2 * k], x[2 * k + 1]), both(-mean[j])), both(rstd[j]));
-                const float2 gk = __fmul2_rn(d2, make_float2(w[2 * k], w[2 * k + 1]));
-                ag[q] = __ffma2_rn(d2, h, ag[q]);
-                ab[q] = __fadd2_rn(ab[q], d2);
-                s1 = __fadd2_rn(s1, gk);
-                s2 = __ffma2_rn(gk, h, s2);
-              }
-            }
-          }
-        }
-      }
-      // both sums at once: the lower half-warp goes on with s1, the upper one with s2
-      const float t1 = s1.x + s1.y, t2 = s2.x + s2.y;
-      float t = (lane & 16) ? t2 : t1;
-      t += __shfl_xor_sync(0xffffffffu, (lane & 16) ? t1 : t2, 16);
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      if ((lane & 15) == 0) sums[j * 2 * warps + (lane >> 4) * warps + warp] = t;
-    }
-    if (g + gridDim.x < ring.groups) stats(g + gridDim.x);
-    bad = __syncthreads_or(!ok);
-    if (bad) break;
-    ring.template release<!KEEP>();
-    if (a.dx) {
-      T* dx = static_cast<T*>(a.dx) + r0 * a.m + c0;
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        const int live = j < rows ? m : 0;
-        // the row's sums over its warps: the lower half-warp s1, the upper one s2
-        const float* mine = sums + j * 2 * warps + (lane >> 4) * warps;
-        const int w = lane & 15;
-        float t;
-        if constexpr (MAXT <= 512) {
-          t = w < warps ? mine[w] : 0.f;
-        } else {   // (loads without a branch: 4096 x 8192 fp32 70 us against 92 us)
-          const float lo = mine[min(w, warps - 1)], hi = mine[min(w + 16, warps - 1)];
-          t = (w < warps ? lo : 0.f) + (w + 16 < warps ? hi : 0.f);
-        }
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        const float c1 = __shfl_sync(0xffffffffu, t, 0) * inv_m;
-        const float c2 = __shfl_sync(0xffffffffu, t, 16) * inv_m;
-        // rstd (g - c1 - xh c2)
-        if constexpr (KEEP) {
-          float2(&h)[P] = xh[j];
-          float2(&d)[P] = gd[j];
-          const float* e = reinterpret_cast<const float*>(d);
-#pragma unroll
-          for (int k = 0; k < P; ++k)
-            d[k] = __fmul2_rn(__ffma2_rn(h[k], both(-c2), __fadd2_rn(d[k], both(-c1))),
-                              both(rstd[j]));
-#pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            float v[V];
-#pragma unroll
-            for (int k = 0; k < V; ++k) v[k] = e[i * V + k];
-            if (c0 + i * step < live) stv<T, V>(dx + j * (int64_t)m + i * step, v);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            const int c = c0 + i * step;
-            if (c < live) {
-              Vec<T, V> vx, vd;
-              float x[V], d[V], w[V];
-              vx.load(px + j * m + i * step);
-              vd.load(pd + j * m + i * step);
-              vx.get(x);
-              vd.get(d);
-              weight(i, w);
-              if constexpr (V == 1) {
-                d[0] = rstd[j] * (d[0] * w[0] - c1 - (x[0] - mean[j]) * rstd[j] * c2);
-              } else {
-#pragma unroll
-                for (int k = 0; k < V / 2; ++k) {
-                  const float2 h = __fmul2_rn(
-                      __fadd2_rn(make_float2(x[2 * k], x[2 * k + 1]), both(-mean[j])),
-                      both(rstd[j]));
-                  float2 e = __ffma2_rn(make_float2(d[2 * k], d[2 * k + 1]),
-                                        make_float2(w[2 * k], w[2 * k + 1]), both(-c1));
-                  e = __fmul2_rn(__ffma2_rn(h, both(-c2), e), both(rstd[j]));
-                  d[2 * k] = e.x;
-                  d[2 * k + 1] = e.y;
-                }
-              }
-              stv<T, V>(dx + j * (int64_t)m + i * step, d);
-            }
-          }
-        }
-      }
-    }
-  }
-  if (bad) {
-    ring.drain();
-    return;
-  }
-  if (!a.part) return;
-  // the block's column sums, its sets of threads added in order; no copy is in flight any more
+// Column sums of a block: E per thread (vector i from column c0 + i step on), added over the sets of
+// threads in order and written once.
+template <int V, int E>
+__device__ __forceinline__ void write_part(const Bwd& a, float* sh, int m, int step, int tid,
+                                           const float* eg, const float* eb) {
   float* out_g = a.part + (int64_t)blockIdx.x * m;
   float* out_b = a.part + ((int64_t)gridDim.x + blockIdx.x) * m;
-  const float* eg = reinterpret_cast<const float*>(ag);
-  const float* eb = reinterpret_cast<const float*>(ab);
-  float* sh = reinterpret_cast<float*>(smem);    // [sets][2][m]
-  __syncthreads();
+  const int c0 = threadIdx.x * V;
+  __syncthreads();   // (the ring's memory: no copy is in flight any more)
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
+  for (int i = 0; i < E / V; ++i) {
     const int c = c0 + i * step;
     if (c < m) {
 #pragma unroll
@@ -921,7 +691,7 @@ __global__ void __launch_bounds__(MAXT, 1) ln_bwd_ring_kernel(const Bwd a, const
     }
   }
   __syncthreads();
-  for (int c = ring.tid(); c < m; c += blockDim.x * blockDim.y) {
+  for (int c = tid; c < m; c += blockDim.x * blockDim.y) {
     float g = 0.f, b = 0.f;
     for (int y = 0; y < (int)blockDim.y; ++y) {
       g += sh[(y * 2) * m + c];
@@ -932,12 +702,316 @@ __global__ void __launch_bounds__(MAXT, 1) ln_bwd_ring_kernel(const Bwd a, const
   }
 }
 
+// Backward, rows of up to 8192 columns. A thread has the same E columns in every row (vector i
+// starts at column (i blockDim.x + threadIdx.x) V), so its shares of dgamma and dbeta and its
+// gammas stay in registers; the block's column sums are written once. A group is R rows for each of
+// blockDim.y sets of threads; per group there is one barrier, which completes the row sums and frees
+// a slot. What is needed again behind the barrier stays in registers: as xh and g (16 a row of
+// E = 8) where a thread may have 128 registers, else as loaded (PACKED).
+// Besides the bytes what counts is instructions and each group's chain (sums, barrier, sums of the
+// warps, dx). So the R rows' 2 R sums are reduced together: each step of the butterfly halves the
+// values that a lane goes on with, until 32 / (2 R) lanes share one, in both levels. And dead columns
+// cost no selects: their threads read the row's first column and have a gamma of zero. 16384 x 4096
+// bf16 takes 76 us so (5.3 TB/s), 89 us with a reduction per row and a select per value. Not kept:
+// two blocks per SM of 256 threads and E = 16 (95 us); two halves of a block one group apart (97 us).
+template <typename T, typename WT, int V, int E, int R, int MAXT, bool PACKED>
+__global__ void __launch_bounds__(MAXT, 1) ln_bwd_kernel(const Bwd a, const RingShape shape) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[kMaxStages];
+  constexpr int N = 2 * R, G = 32 / N;            // row sums of a set; lanes that share one
+  __shared__ float buf[2][MAXT / 32 * N];         // [set][sum][warp]
+  __shared__ int abort_flag;
+  constexpr int NV = E / V, P = E / 2;
+  const int m = (int)a.m, warps = blockDim.x >> 5, step = blockDim.x * V;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Ring<T, V, 2> ring;
+  ring.src[0] = static_cast<const char*>(a.x);
+  ring.src[1] = static_cast<const char*>(a.dy);
+  ring.init(smem, full, &abort_flag, a.err, shape, a.T, a.m, blockDim.y * R);
+  pdl_wait();
+  pdl_trigger();
+  ring.start();
+  const int c0 = threadIdx.x * V;
+  int off[NV];                                    // columns as read
+  float2 gm[P], ag[P], ab[P];
+  {
+    const WT* gamma = static_cast<const WT*>(a.gamma);
+    float* e = reinterpret_cast<float*>(gm);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const bool in = c0 + i * step < m;
+      off[i] = in ? c0 + i * step : 0;
+      float v[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[k] = 0.f;
+      if (in) ldw<WT, V>(gamma, off[i], 1.f, v);
+#pragma unroll
+      for (int k = 0; k < V; ++k) e[i * V + k] = v[k];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < P; ++k) ag[k] = ab[k] = both(0.f);
+  float mean_n[R], rstd_n[R];                // of the next group's rows
+  auto stats = [&](int64_t r, int64_t left) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      mean_n[j] = j < left ? __ldg(a.mean + r + j) : 0.f;
+      rstd_n[j] = j < left ? __ldg(a.rstd + r + j) : 0.f;
+    }
+  };
+  int64_t r0 = (int64_t)blockIdx.x * ring.rows + threadIdx.y * R;
+  const int64_t hop = (int64_t)gridDim.x * ring.rows;
+  stats(r0, a.T - r0);
+  // a row's vectors as fp32 pairs
+  auto unpack = [](const Vec<T, V> (&u)[NV], float2 (&f)[P]) {
+    float* e = reinterpret_cast<float*>(f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float v[V];
+      u[i].get(v);
+#pragma unroll
+      for (int k = 0; k < V; ++k) e[i * V + k] = v[k];
+    }
+  };
+  const float inv_m = 1.f / (float)m;
+  bool bad = false;
+  int turn = 0;
+  for (int64_t g = blockIdx.x; g < ring.groups; g += gridDim.x, r0 += hop) {
+    const int rows = a.T - r0 >= R ? R : max(0, (int)(a.T - r0));   // (r0 < T + the group's rows)
+    float2 mean[R], rstd[R];                 // -mean, rstd
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      mean[j] = both(-mean_n[j]);
+      rstd[j] = both(rstd_n[j]);
+    }
+    const bool ok = ring.wait(g);
+    Vec<T, V> x[R][NV], d[R][NV];
+    if (rows == R) {
+      const T* px = ring.row(g, 0) + threadIdx.y * R * m;
+      const T* pd = ring.row(g, 1) + threadIdx.y * R * m;
+#pragma unroll
+      for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          x[j][i].load(px + j * m + off[i]);
+          d[j][i].load(pd + j * m + off[i]);
+        }
+    } else {   // rows past the last one: some row's x and a dy of zero add nothing
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const int r = j < rows ? threadIdx.y * R + j : 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          x[j][i].load(ring.row(g, 0) + r * m + off[i]);
+          if (j < rows) d[j][i].load(ring.row(g, 1) + r * m + off[i]);
+          else d[j][i].clear();
+        }
+      }
+    }
+    float2 xh[R][P], gd[R][P];
+    float s[N];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      float2 s1 = both(0.f), s2 = both(0.f);
+      unpack(x[j], xh[j]);
+      unpack(d[j], gd[j]);
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        float2& h = xh[j][k];
+        float2& q = gd[j][k];
+        h = __fmul2_rn(__fadd2_rn(h, mean[j]), rstd[j]);
+        ag[k] = __ffma2_rn(q, h, ag[k]);
+        ab[k] = __fadd2_rn(ab[k], q);
+        q = __fmul2_rn(q, gm[k]);
+        s1 = __fadd2_rn(s1, q);
+        s2 = __ffma2_rn(q, h, s2);
+      }
+      s[2 * j] = s1.x + s1.y;
+      s[2 * j + 1] = s2.x + s2.y;
+    }
+    // lane l ends with the warp's sum l / G
+    int o = 16;
+#pragma unroll
+    for (int n = N / 2; n >= 1; n >>= 1, o >>= 1) {
+      const bool up = lane & o;
+#pragma unroll
+      for (int k = 0; k < n; ++k) {
+        const float give = up ? s[k] : s[k + n];
+        s[k] = (up ? s[k + n] : s[k]) + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+    }
+#pragma unroll
+    for (int q = G / 2; q > 0; q >>= 1) s[0] += __shfl_xor_sync(0xffffffffu, s[0], q);
+    float* mine = buf[turn] + (threadIdx.y * N + lane / G) * warps;   // (the other may still be read)
+    turn ^= 1;
+    if (lane % G == 0) mine[warp] = s[0];
+    stats(r0 + hop, a.T - r0 - hop);
+    bad = __syncthreads_or(!ok);
+    if (bad) break;
+    ring.release();
+    if (a.dx) {
+      float t = 0.f;
+#pragma unroll
+      for (int w = 0; w < MAXT / 32; w += G)
+        if (w + lane % G < warps) t += mine[w + lane % G];
+#pragma unroll
+      for (int q = G / 2; q > 0; q >>= 1) t += __shfl_xor_sync(0xffffffffu, t, q);
+      t *= -inv_m;
+      T* dx = static_cast<T*>(a.dx) + r0 * a.m;
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const float2 c1 = both(__shfl_sync(0xffffffffu, t, 2 * j * G));
+        const float2 c2 = both(__shfl_sync(0xffffffffu, t, (2 * j + 1) * G));
+        if constexpr (PACKED) {
+          unpack(x[j], xh[j]);
+          unpack(d[j], gd[j]);
+        }
+        // rstd (g - c1 - xh c2)
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          float2& h = xh[j][k];
+          float2& q = gd[j][k];
+          if constexpr (PACKED) {
+            h = __fmul2_rn(__fadd2_rn(h, mean[j]), rstd[j]);
+            q = __ffma2_rn(q, gm[k], c1);
+          } else {
+            q = __fadd2_rn(q, c1);
+          }
+          q = __fmul2_rn(__ffma2_rn(h, c2, q), rstd[j]);
+        }
+        const float* e = reinterpret_cast<const float*>(gd[j]);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          float v[V];
+#pragma unroll
+          for (int k = 0; k < V; ++k) v[k] = e[i * V + k];
+          if (j < rows && c0 + i * step < m) stv<T, V>(dx + j * m + off[i], v);
+        }
+      }
+    }
+  }
+  if (bad) {
+    ring.drain();
+    return;
+  }
+  if (a.part)
+    write_part<V, E>(a, reinterpret_cast<float*>(smem), m, step, ring.tid(),
+                     reinterpret_cast<const float*>(ag), reinterpret_cast<const float*>(ab));
+}
+
+// The same for rows of 8193 columns and more: one row a group, E = 32 columns per thread; the row is
+// read from its slot a second time, which is freed one group later, and gamma comes from L1.
+template <typename T, typename WT, int V>
+__global__ void __launch_bounds__(512, 1) ln_bwd_wide_kernel(const Bwd a, const RingShape shape) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ float buf[2][2][16];                 // [sum][warp]
+  __shared__ int abort_flag;
+  constexpr int E = 32, NV = E / V;
+  const int m = (int)a.m, warps = blockDim.x >> 5, step = blockDim.x * V;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Ring<T, V, 2> ring;
+  ring.src[0] = static_cast<const char*>(a.x);
+  ring.src[1] = static_cast<const char*>(a.dy);
+  ring.init(smem, full, &abort_flag, a.err, shape, a.T, a.m, 1);
+  pdl_wait();
+  pdl_trigger();
+  ring.start();
+  const WT* gamma = static_cast<const WT*>(a.gamma);
+  const int c0 = threadIdx.x * V;
+  float ag[E], ab[E];
+#pragma unroll
+  for (int k = 0; k < E; ++k) ag[k] = ab[k] = 0.f;
+  const float inv_m = 1.f / (float)m;
+  float mean_n = __ldg(a.mean + blockIdx.x), rstd_n = __ldg(a.rstd + blockIdx.x);
+  bool bad = false;
+  int turn = 0;
+  for (int64_t r = blockIdx.x; r < a.T; r += gridDim.x) {
+    const float mean = mean_n, rstd = rstd_n;
+    const bool ok = ring.wait(r);
+    const T* px = ring.row(r, 0) + c0;
+    const T* pd = ring.row(r, 1) + c0;
+    float(*sums)[16] = buf[turn];                 // (the other one may still be read)
+    turn ^= 1;
+    // vector i: xh and g, and dy
+    auto get = [&](int i, float (&h)[V], float (&gk)[V], float (&d)[V]) {
+      Vec<T, V> vx, vd;
+      vx.load(px + i * step);
+      vd.load(pd + i * step);
+      vx.get(h);
+      vd.get(d);
+      ldw<WT, V>(gamma, c0 + i * step, 1.f, gk);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        h[k] = (h[k] - mean) * rstd;
+        gk[k] *= d[k];
+      }
+    };
+    float s1[2] = {0.f, 0.f}, s2[2] = {0.f, 0.f};   // (two chains of sums each)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (c0 + i * step < m) {
+        float h[V], gk[V], d[V];
+        get(i, h, gk, d);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const int q = i * V + k;
+          ag[q] += d[k] * h[k];
+          ab[q] += d[k];
+          s1[q & 1] += gk[k];
+          s2[q & 1] += gk[k] * h[k];
+        }
+      }
+    }
+    // both sums at once: the lower half-warp goes on with s1, the upper one with s2
+    const float t1 = s1[0] + s1[1], t2 = s2[0] + s2[1];
+    float t = (lane & 16) ? t2 : t1;
+    t += __shfl_xor_sync(0xffffffffu, (lane & 16) ? t1 : t2, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if ((lane & 15) == 0) sums[lane >> 4][warp] = t;
+    if (r + gridDim.x < a.T) {
+      mean_n = __ldg(a.mean + r + gridDim.x);
+      rstd_n = __ldg(a.rstd + r + gridDim.x);
+    }
+    bad = __syncthreads_or(!ok);
+    if (bad) break;
+    ring.release_before();
+    if (a.dx) {
+      t = (lane & 15) < warps ? sums[lane >> 4][lane & 15] : 0.f;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      const float c1 = __shfl_sync(0xffffffffu, t, 0) * inv_m;
+      const float c2 = __shfl_sync(0xffffffffu, t, 16) * inv_m;
+      T* dx = static_cast<T*>(a.dx) + r * a.m + c0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (c0 + i * step < m) {
+          float h[V], gk[V], d[V];
+          get(i, h, gk, d);
+#pragma unroll
+          for (int k = 0; k < V; ++k) d[k] = rstd * (gk[k] - c1 - h[k] * c2);
+          stv<T, V>(dx + i * step, d);
+        }
+      }
+    }
+  }
+  if (bad) {
+    ring.drain();
+    return;
+  }
+  if (a.part)
+    write_part<V, E>(a, reinterpret_cast<float*>(smem), m, step, ring.tid(), ag, ab);
+}
+
 constexpr int kMaxParts = 148;   // one block per SM
 
 // Shape of the one-pass backward for a width; stages < 2: a row is too wide for the ring. E = 8 up to
-// 8192 columns (a row then has at most 1024 threads), 32 beyond. `sets` sets of threads and R rows
-// each make a group: at most 64 KB of x and dy (three slots in flight), no more than leaves a group
-// for every SM; R up to 4 in blocks of 512 threads, 2 in larger ones.
+// 5120 columns (at most 640 threads of 96 registers), 16 up to 8192 (8192 x 8192 bf16 86 us; 1024
+// threads of 8 columns and 64 registers spill: 145 us), 32 beyond. `sets` sets of threads and R rows
+// each make a group: at most 96 KB of x and dy, no more than leaves a group for every SM. R = 2 with
+// E = 8 (8192 x 5120 bf16 58.5 us against 67 us of one row; four rows spill: 16384 x 4096 bf16
+// 92 us against 76 us), one row with E = 16 (8192 x 8192 bf16 two rows: 107 us).
 struct GroupShape {
   int threads, sets, E, R;
   RingShape ring;
@@ -945,15 +1019,15 @@ struct GroupShape {
 };
 GroupShape group_shape(int64_t T, int64_t m, int esz) {
   GroupShape sh;
-  sh.E = m <= 8192 ? 8 : 32;
+  sh.E = m <= 5120 ? 8 : m <= 8192 ? 16 : 32;
   sh.threads = 32 * (int)((m + 32 * sh.E - 1) / (32 * sh.E));
-  const int most = sh.E == 32 ? 1 : sh.threads > 512 ? 2 : 4;
-  const int64_t fit = 64 * 1024 / (2 * m * esz);                  // rows in 64 KB
+  const int most = sh.E == 8 ? 2 : 1;
+  const int64_t fit = 96 * 1024 / (2 * m * esz);                  // rows in 64 KB
   const int64_t share = (T + kMaxParts - 1) / kMaxParts;          // rows per SM
   const int64_t rows = std::max<int64_t>(1, std::min(fit, share));
   sh.R = most;
   while (sh.R > rows) sh.R /= 2;
-  const int block = most == 4 ? 512 : sh.threads;
+  const int block = std::max(sh.threads, 512);
   sh.sets = (int)std::max<int64_t>(1, std::min<int64_t>(block / sh.threads, rows / sh.R));
   // the window around unaligned rows needs up to 30 bytes more
   sh.ring.slot = (int)(((int64_t)sh.sets * sh.R * m * esz + 31) / 16 * 16);
@@ -964,9 +1038,8 @@ GroupShape group_shape(int64_t T, int64_t m, int esz) {
   return sh;
 }
 
-template <typename T, typename WT, int V, int E, int R, int MAXT, bool KEEP>
-cudaError_t launch_bwd_er(const Bwd& a, const GroupShape& sh, cudaStream_t s) {
-  auto kern = ln_bwd_ring_kernel<T, WT, V, E, R, MAXT, KEEP>;
+template <typename K>
+cudaError_t launch_ring(K kern, const Bwd& a, const GroupShape& sh, cudaStream_t s) {
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem);
   if (e != cudaSuccess) return e;
@@ -975,14 +1048,13 @@ cudaError_t launch_bwd_er(const Bwd& a, const GroupShape& sh, cudaStream_t s) {
 }
 template <typename T, typename WT, int V>
 cudaError_t launch_bwd(const Bwd& a, const GroupShape& sh, cudaStream_t s) {
-  if (sh.E == 32) return launch_bwd_er<T, WT, V, 32, 1, 512, false>(a, sh, s);
-  if (sh.threads <= 512) {
-    if (sh.R == 4) return launch_bwd_er<T, WT, V, 8, 4, 512, true>(a, sh, s);
-    if (sh.R == 2) return launch_bwd_er<T, WT, V, 8, 2, 512, true>(a, sh, s);
-    return launch_bwd_er<T, WT, V, 8, 1, 512, true>(a, sh, s);
-  }
-  return sh.R == 2 ? launch_bwd_er<T, WT, V, 8, 2, 1024, false>(a, sh, s)
-                   : launch_bwd_er<T, WT, V, 8, 1, 1024, true>(a, sh, s);
+  if (sh.E == 32) return launch_ring(ln_bwd_wide_kernel<T, WT, V>, a, sh, s);
+  if (sh.E == 16) return launch_ring(ln_bwd_kernel<T, WT, V, 16, 1, 512, true>, a, sh, s);
+  if (sh.threads > 512)
+    return sh.R == 2 ? launch_ring(ln_bwd_kernel<T, WT, V, 8, 2, 640, true>, a, sh, s)
+                     : launch_ring(ln_bwd_kernel<T, WT, V, 8, 1, 640, true>, a, sh, s);
+  return sh.R == 2 ? launch_ring(ln_bwd_kernel<T, WT, V, 8, 2, 512, false>, a, sh, s)
+                   : launch_ring(ln_bwd_kernel<T, WT, V, 8, 1, 512, false>, a, sh, s);
 }
 
 int row_blocks(int64_t T) { return (int)std::min<int64_t>(T, 148 * 8); }
