@@ -52,7 +52,6 @@ constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kRegsLaunch = 168, kRegsIssue = 56, kRegsEpi = 224;
 static_assert(128 * kRegsIssue + 32 * kEpiWarps * kRegsEpi <= kThreads * kRegsLaunch,
               "the register split must fit the launch's registers");
-constexpr int kChunk = 2;                  // K blocks per accumulator of an fp32 result
 constexpr int kPiece = 4096;               // 32 rows x 64 columns of fp16
 constexpr int kEpiStage = 2 * kPiece;      // per epilogue warp
 // Tile numbers handed from the producer to the others. The producer is at most two tiles (the
@@ -81,7 +80,7 @@ struct Job {
   Kind k[3];
   int batch, steps, per_step, total;   // tiles per step (all matrices) and in all
   int R;                               // padded rows of every result
-  int exact;
+  int exact, chunk;                    // chunk: K blocks per accumulator of an fp32 result
   int fmode, out_f32, vec;             // the caller's array: layout, type, rows start on 16 bytes
   void* out;
   long long um, un;                    // its rows and columns (of the result as computed)
@@ -132,10 +131,10 @@ __device__ __forceinline__ int segments(const Job& j, const Work& w) {
 }
 __device__ __forceinline__ int part_a(int n, int seg) { return n == 3 && seg == 0; }
 __device__ __forceinline__ int part_b(int n, int seg) { return n > 1 && seg == n - 2; }
-// K blocks that the first accumulator of a tile sums: the small products and the first kChunk of the
-// large one for fp32 results, everything otherwise
+// K blocks that the first accumulator of a tile sums: the small products and the first job.chunk of
+// the large one for fp32 results, everything otherwise
 __device__ __forceinline__ int head_blocks(const Job& j, int n, int nk) {
-  return j.exact ? (n - 1) * nk + min(kChunk, nk) : n * nk;
+  return j.exact ? (n - 1) * nk + min(j.chunk, nk) : n * nk;
 }
 
 template <int CG>
@@ -354,7 +353,7 @@ __device__ __forceinline__ void emit_user(const Job& p, const float* v, float f,
 // The tensor core adds to its fp32 accumulator without rounding to nearest: every 16-deep step
 // loses up to a whole unit in the last place, always towards zero, and K = 2048 in three
 // passes came out 3.8e-5 off. So the parts' small products (hi lo, lo hi) come first, and for fp32
-// results an accumulator of large products sums only kChunk K blocks; the epilogue warps add the
+// results an accumulator of large products sums only job.chunk K blocks; the epilogue warps add the
 // accumulators in registers (round to nearest) while the next one fills.
 // Every wait is bounded; on expiry the device error word is set, the roles leave their loops,
 // copies and MMAs in flight are waited for (bounded) and TMEM is freed.
@@ -555,7 +554,7 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
           const uint32_t bstep = mn ? 2048u >> 4 : 32u >> 4;
           const uint32_t a_lo = desc_lo(smem_u32(sa), 16), b_lo = desc_lo(smem_u32(sb), mn ? 64 * BK * 2 : 16);
           for (int kb = 0, end = head_blocks(job, ns, nk1); ok && kb < nk;
-               end = min(nk, end + kChunk), ++count) {
+               end = min(nk, end + job.chunk), ++count) {
             const int acc = count & 1;
             ok = wait_inline(smem_u32(tempty + acc), ((uint32_t)(count >> 1) & 1u) ^ 1u, ctl, kErrMma);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -627,7 +626,7 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
       float v[COLS];
 #pragma unroll
       for (int q = 0; q < COLS; ++q) v[q] = 0.f;
-      for (int done = 0; done < nk; done = done ? done + kChunk : head, ++count) {
+      for (int done = 0; done < nk; done = done ? done + job.chunk : head, ++count) {
         const int acc = count & 1;
         ok = wait_inline(smem_u32(tfull + acc), (uint32_t)(count >> 1) & 1u, ctl, kErrEpilogue);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -1185,6 +1184,12 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
   job.total = job.per_step * p.steps;
   job.R = (int)d.R;
   job.exact = exact;
+  // A truncated accumulator of 128 terms shrinks what is summed of one sign by 2^-18 or so. Of matrices
+  // with many rows the result hardly feels it (640 x 2000: 0.9 times the error of fp32 products,
+  // 2048 x 2048 0.5 times); with up to 512, whose spectrum is narrow, it was up to twice that error
+  // (500 x 260), and 64 terms an accumulator bring it to 1.2 times for 6 to 11 % more time (200 ->
+  // 213 us for 3 of 1000 x 333; 2048 x 2048 would take 620 -> 690 us).
+  job.chunk = d.R <= 512 ? 1 : 2;
   job.fmode = skew ? kPacked : d.tall ? kTransposed : kRows;
   job.out = out;
   job.out_f32 = exact;

@@ -2,7 +2,7 @@
 // one CTA per matrix and one launch for everything. X, A and B stay in shared memory as fp16 parts
 // in the tensor core's operand layouts, accumulators in tensor memory; the formulas, scales, part
 // products and their order are those of orth.cu, whose fifteen dependent products cost about 6 us
-// each in round trips through L2 (100 us for 16 blocks of 64; here the time of one matrix).
+// each in round trips through L2 (100 us for 16 blocks of 64; here 28 us, the time of one matrix).
 //
 // An operand is 128 rows x 128 columns per part: two chunks of 64 columns, 128 rows of 128 bytes
 // each, 16-byte unit u of row i at u ^ (i & 7). As a left or right operand of gram and square, and
@@ -20,6 +20,13 @@ constexpr int kThreads = kNormThreads;               // eight warps
 constexpr uint32_t kChunkBytes = 128 * 128;          // 128 rows x 64 columns
 constexpr uint32_t kPartBytes = 2 * kChunkBytes;     // one part of one operand
 constexpr uint32_t kOperandBytes = 2 * kPartBytes;
+// For fp32 results the large product is summed in several accumulators, four of 16 of K = 64 or two of
+// 64 of K = 128, and those are added in registers: the tensor core truncates what it adds (see
+// ns_kernel in orth.cu). Blocks of 32, 64, 128: 1.3, 0.8, 1.1 times the error of fp32 products; with
+// one accumulator 1.5, 1.4, 1.7 times in 3 to 10 % less time (16 blocks of 64 27.1 us against 28.0,
+// 3 of 128 42.6 us against 47.3).
+constexpr int kMostAccs = 4;
+constexpr uint32_t kTmemCols = kSmallSide * kMostAccs;
 constexpr int kOutLd = kSmallSide + 1;               // staged results: floats per row
 constexpr size_t kSmem = 3 * kOperandBytes + 1024;
 static_assert((size_t)kSmallSide * kOutLd * sizeof(float) <= 2 * kOperandBytes,
@@ -39,6 +46,32 @@ struct Small {
 __device__ __forceinline__ uint32_t at16(int i, int j) {   // byte of element (i, j) in a part
   return (uint32_t)(j >> 6) * kChunkBytes + (uint32_t)i * 128 +
          ((((uint32_t)(j >> 3) & 7u) ^ ((uint32_t)i & 7u)) << 4) + ((uint32_t)j & 7u) * 2;
+}
+
+// 32 columns of an accumulator on their way into registers, which tmem_arrived() hands out
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 
 __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_constant__ Small p) {
@@ -65,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&tmem_holder)),
-                 "r"(128u)
+                 "r"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -110,9 +143,10 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
   tc_fence_after();
   const uint32_t tmem = tmem_holder;
 
-  const int quarter = warp & 3, c0 = (warp >> 2) * 64;   // this warp's rows and columns of a result
+  // this warp's rows of a result; of its columns the first or the second half
+  const int quarter = warp & 3, half = warp >> 2;
   const int row = quarter * 32 + lane;
-  const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c0;
+  const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
   uint32_t phase = 0;
   bool ok = true;
   for (int q = 0; ok && q < 3 * p.steps; ++q) {
@@ -121,6 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
     const int N = kind == kUpdate ? ld : R, K = kind == kGram ? ld : R;
     if (warp == 0) {
       const int ns = p.exact ? 3 : kind == kUpdate && !last ? 2 : 1;
+      const int deep = K == 64 ? 4 : 6;   // 16 or 64 of K an accumulator
       const uint32_t id = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24) |
                           (kind == kUpdate ? 1u << 16 : 0u);
       const uint32_t sa = smem_u32(kind == kGram ? X : kind == kSquare ? A : B);
@@ -134,7 +169,11 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
           const uint32_t a = desc_lo(sa + pa + kmaj, 16);
           const uint32_t b = kind == kUpdate ? desc_lo(sb + pb + (uint32_t)k * 128, kChunkBytes)
                                              : desc_lo(sb + pb + kmaj, 16);
-          if (elect_one()) mma<1>(tmem, a, b, id, (seg > 0 || k > 0) ? 1u : 0u);
+          // the small products and the first part of the large one share an accumulator
+          const int acc = p.exact && seg == ns - 1 ? k >> deep : 0;
+          const bool more = acc > 0 ? (k & ((1 << deep) - 1)) > 0 : seg > 0 || k > 0;
+          if (elect_one())
+            mma<1>(tmem + (uint32_t)(acc * kSmallSide), a, b, id, more ? 1u : 0u);
         }
       }
       if (elect_one()) umma_commit(smem_u32(&done_bar));
@@ -144,58 +183,75 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
     ok = __syncthreads_and(ok);
     if (!ok) break;
     tc_fence_after();
-    // columns past the result's padded width are not computed
-    if (c0 < N) {
-      float v[64];
+    // columns past the result's padded width N (64 or 128) are not computed
+    const float f = p.f[kind][t], fa = p.fa[t], da = p.da[t];
+    for (int c0 = half * (N / 2); c0 < (half + 1) * (N / 2); c0 += 32) {
+      float v[32];
+      {
+        uint32_t r[kMostAccs][32];
+        const int accs = !p.exact ? 1 : K == 64 ? 4 : 2;
+        tmem_ld32_start(trow + (uint32_t)c0, r[0]);
+        if (accs > 1) tmem_ld32_start(trow + (uint32_t)(kSmallSide + c0), r[1]);
+        if (accs > 2) {
+          tmem_ld32_start(trow + (uint32_t)(2 * kSmallSide + c0), r[2]);
+          tmem_ld32_start(trow + (uint32_t)(3 * kSmallSide + c0), r[3]);
+        }
+        tmem_arrived(r[0]);
 #pragma unroll
-      for (int c = 0; c < 64; c += 32) {
-        uint32_t r[32];
-        tmem_ld32(trow + (uint32_t)c, r);
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[0][i]);
+        if (accs > 1) {
+          tmem_arrived(r[1]);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[c + i] = __uint_as_float(r[i]);
+          for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(r[1][i]);
+        }
+        if (accs > 2) {
+          tmem_arrived(r[2]);
+          tmem_arrived(r[3]);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            v[i] += __uint_as_float(r[2][i]) + __uint_as_float(r[3][i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= f;
       }
-      const float f = p.f[kind][t];
       if (out) {
         float* stage = reinterpret_cast<float*>(A);
 #pragma unroll
-        for (int c = 0; c < 64; ++c) stage[row * kOutLd + c0 + c] = v[c] * f;
-      } else {
-        uint8_t* to = kind == kGram ? A : kind == kSquare ? B : X;
-        const float fa = p.fa[t], da = p.da[t];
+        for (int c = 0; c < 32; ++c) stage[row * kOutLd + c0 + c] = v[c];
+        continue;
+      }
+      uint8_t* to = kind == kGram ? A : kind == kSquare ? B : X;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const uint32_t at = at16(row, c0 + 8 * u);
-          float e[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) e[i] = v[8 * u + i] * f;
-          if (kind == kSquare) {   // + fa A + da I
-            const uint4 h = *reinterpret_cast<const uint4*>(A + at);
-            const uint4 l = *reinterpret_cast<const uint4*>(A + kPartBytes + at);
-            const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 a2 = __half22float2(*reinterpret_cast<const __half2*>(&hw[i]));
-              const float2 b2 = p.exact ? __half22float2(*reinterpret_cast<const __half2*>(&lw[i]))
-                                        : make_float2(0.f, 0.f);
-              e[2 * i] += (a2.x + b2.x) * fa;
-              e[2 * i + 1] += (a2.y + b2.y) * fa;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (row == c0 + 8 * u + i) e[i] += da;
-          }
-          uint32_t h[4], l[4];
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t at = at16(row, c0 + 8 * u);
+        float* e = v + 8 * u;
+        if (kind == kSquare) {   // + fa A + da I
+          const uint4 h = *reinterpret_cast<const uint4*>(A + at);
+          const uint4 l = *reinterpret_cast<const uint4*>(A + kPartBytes + at);
+          const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const __half2 w = __floats2half2_rn(e[2 * i], e[2 * i + 1]);
-            const __half2 z =
-                __floats2half2_rn(e[2 * i] - __low2float(w), e[2 * i + 1] - __high2float(w));
-            h[i] = *reinterpret_cast<const uint32_t*>(&w);
-            l[i] = *reinterpret_cast<const uint32_t*>(&z);
+            const float2 a2 = __half22float2(*reinterpret_cast<const __half2*>(&hw[i]));
+            const float2 b2 = p.exact ? __half22float2(*reinterpret_cast<const __half2*>(&lw[i]))
+                                      : make_float2(0.f, 0.f);
+            e[2 * i] += (a2.x + b2.x) * fa;
+            e[2 * i + 1] += (a2.y + b2.y) * fa;
           }
-          *reinterpret_cast<uint4*>(to + at) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(to + kPartBytes + at) = make_uint4(l[0], l[1], l[2], l[3]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (row == c0 + 8 * u + i) e[i] += da;
         }
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __half2 w = __floats2half2_rn(e[2 * i], e[2 * i + 1]);
+          const __half2 z =
+              __floats2half2_rn(e[2 * i] - __low2float(w), e[2 * i + 1] - __high2float(w));
+          h[i] = *reinterpret_cast<const uint32_t*>(&w);
+          l[i] = *reinterpret_cast<const uint32_t*>(&z);
+        }
+        *reinterpret_cast<uint4*>(to + at) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(to + kPartBytes + at) = make_uint4(l[0], l[1], l[2], l[3]);
       }
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -222,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(128u)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
                  : "memory");
   }
 }
