@@ -10,7 +10,8 @@
 // deviations' own mean dm corrects the first one's rounding: mean = first + dm,
 // var = sum d^2 / m - dm^2, x - mean = d - dm. Column sums are taken
 // per range of rows and the ranges added in order: no atomics, the same bits on every run.
-// Memory bound: each kernel reads its inputs once from HBM.
+// Memory bound: each kernel reads its inputs once from HBM. No input is read through the read-only
+// cache: a block may start before the kernel that writes the input has ended.
 #include "norm.h"
 #include "umma_ptx.cuh"
 
@@ -755,8 +756,8 @@ __global__ void __launch_bounds__(MAXT, 1) ln_bwd_kernel(const Bwd a, const Ring
   auto stats = [&](int64_t r, int64_t left) {
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-      mean_n[j] = j < left ? __ldg(a.mean + r + j) : 0.f;
-      rstd_n[j] = j < left ? __ldg(a.rstd + r + j) : 0.f;
+      mean_n[j] = j < left ? a.mean[r + j] : 0.f;
+      rstd_n[j] = j < left ? a.rstd[r + j] : 0.f;
     }
   };
   int64_t r0 = (int64_t)blockIdx.x * ring.rows + threadIdx.y * R;
@@ -923,7 +924,7 @@ __global__ void __launch_bounds__(512, 1) ln_bwd_wide_kernel(const Bwd a, const 
 #pragma unroll
   for (int k = 0; k < E; ++k) ag[k] = ab[k] = 0.f;
   const float inv_m = 1.f / (float)m;
-  float mean_n = __ldg(a.mean + blockIdx.x), rstd_n = __ldg(a.rstd + blockIdx.x);
+  float mean_n = a.mean[blockIdx.x], rstd_n = a.rstd[blockIdx.x];
   bool bad = false;
   int turn = 0;
   for (int64_t r = blockIdx.x; r < a.T; r += gridDim.x) {
@@ -971,8 +972,8 @@ __global__ void __launch_bounds__(512, 1) ln_bwd_wide_kernel(const Bwd a, const 
     for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     if ((lane & 15) == 0) sums[lane >> 4][warp] = t;
     if (r + gridDim.x < a.T) {
-      mean_n = __ldg(a.mean + r + gridDim.x);
-      rstd_n = __ldg(a.rstd + r + gridDim.x);
+      mean_n = a.mean[r + gridDim.x];
+      rstd_n = a.rstd[r + gridDim.x];
     }
     bad = __syncthreads_or(!ok);
     if (bad) break;

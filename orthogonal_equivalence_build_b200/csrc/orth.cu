@@ -743,10 +743,11 @@ int norm_chunks(int64_t elems) {
 }
 
 // partial[g][chunk] = sum of the chunk's squares, in 64 bits: an fp32 square overflows at 1.8e19
-// and vanishes at 1e-23, both of which are ordinary fp32 and bf16 values.
+// and vanishes at 1e-23, both of which are ordinary fp32 and bf16 values. (Plain loads: a block may
+// start before the kernel that writes x has ended.)
 __global__ void __launch_bounds__(kNormThreads)
-ns_norm_kernel(const void* __restrict__ x, int f32, int vec, long long elems, int chunks,
-               double* __restrict__ partial, int* __restrict__ counts, int ncounts) {
+ns_norm_kernel(const void* x, int f32, int vec, long long elems, int chunks, double* partial,
+               int* counts, int ncounts) {
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x == 0 && blockIdx.y == 0)   // the products' counters start at zero
@@ -760,14 +761,14 @@ ns_norm_kernel(const void* __restrict__ x, int f32, int vec, long long elems, in
       const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + base);
 #pragma unroll 4
       for (long long i = lo / 4 + threadIdx.x; i < hi / 4; i += kNormThreads) {
-        const float4 v = __ldg(p + i);
+        const float4 v = p[i];
         s += (double)v.x * v.x + (double)v.y * v.y + (double)v.z * v.z + (double)v.w * v.w;
       }
     } else {
       const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) + base);
 #pragma unroll 4
       for (long long i = lo / 8 + threadIdx.x; i < hi / 8; i += kNormThreads) {
-        const uint4 v = __ldg(p + i);
+        const uint4 v = p[i];
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {

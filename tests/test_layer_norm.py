@@ -312,6 +312,30 @@ def test_graph_replay_and_other_stream():
             assert torch.equal(o, w)
 
 
+@gpu
+@pytest.mark.parametrize("m", [512, 1021, 8192, 12000])
+def test_inputs_written_by_the_launch_before(m):
+    """Forward and backward in place, over and over: every launch reads what the one before wrote."""
+    x, dy, gamma, beta = make(301, m, "f32", "f32")
+    mean, rstd = torch.empty(301, device="cuda"), torch.empty(301, device="cuda")
+    dg, db = torch.empty(m, device="cuda"), torch.empty(m, device="cuda")
+
+    def chain(wait):
+        a, d = x.clone(), dy.clone()
+        torch.cuda.synchronize()
+        for _ in range(10):
+            poetx.layer_norm_fwd(a, gamma, beta, a, mean, rstd)
+            if wait:
+                torch.cuda.synchronize()
+            poetx.layer_norm_bwd(a, d, gamma, mean, rstd, d, dg, db)
+            if wait:
+                torch.cuda.synchronize()
+        return a, d, mean.clone(), rstd.clone(), dg.clone(), db.clone()
+
+    for got, want in zip(chain(False), chain(True)):
+        assert torch.equal(got, want)
+
+
 # ----------------------------------------------------------------------------- refusals (CPU)
 @pytest.mark.parametrize("kw,status", [
     (dict(x=None), 1), (dict(y=None), 1), (dict(T=-1), 1), (dict(m=-1), 1), (dict(eps=-1e-5), 1),

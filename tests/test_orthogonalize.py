@@ -299,6 +299,53 @@ def test_graph_replay_and_other_stream():
 
 
 @gpu
+def test_graphs_that_share_a_workspace():
+    xs = [torch.randn(300, 520, device="cuda"), torch.randn(700, 640, device="cuda")]
+    refs, outs = ([torch.empty_like(x) for x in xs] for _ in range(2))
+    for x, r in zip(xs, refs):
+        poetx.orthogonalize(x, r)
+    ws = torch.empty(max(poetx.orthogonalize_workspace_bytes(x, x) for x in xs),
+                     dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in xs]
+    for g, x, o in zip(graphs, xs, outs):
+        with torch.cuda.graph(g):
+            poetx.orthogonalize(x, o, workspace=ws)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for o, r in zip(outs, refs):
+            assert torch.equal(o, r)
+    poetx.device_status()
+
+
+@gpu
+def test_an_input_written_by_the_launch_before():
+    """A chain of calls whose inputs the call before has just written, with no wait in between."""
+    x = torch.randn(4, 100 * 99 // 2, device="cuda")
+    a, b = x.clone(), x.clone()
+    for _ in range(20):
+        poetx.orthogonalize_q(a, 100, a)
+        poetx.orthogonalize_q(b, 100, b)
+        torch.cuda.synchronize()
+    c = x.clone()
+    for _ in range(20):
+        poetx.orthogonalize_q(c, 100, c)
+    assert torch.equal(a, c) and torch.equal(b, c)
+    y = torch.randn(2, 300, 520, device="cuda")
+    d, e = y.clone(), y.clone()
+    for _ in range(10):
+        poetx.orthogonalize(d, d)
+        torch.cuda.synchronize()
+    for _ in range(10):
+        poetx.orthogonalize(e, e)
+    assert torch.equal(d, e)
+
+
+@gpu
 def test_two_streams_at_once():
     xs = [torch.randn(512, 640, device="cuda") for _ in range(2)]
     refs = [torch.empty_like(x) for x in xs]
