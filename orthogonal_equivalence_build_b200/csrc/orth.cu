@@ -62,12 +62,15 @@ constexpr int kSlots = 8;
 // ------------------------------------------------------------------ the work
 // Tile shapes. CG = 1: 128 x 128 tiles of one CTA; CG = 2: 256 x 256 tiles of a CTA pair
 // (cta_group::2: each CTA holds 128 rows of A, half of B's columns and 128 rows of the result).
-template <int CG_>
+// TN = 64: 128 x 64 tiles of one CTA, whose epilogue is the first four warps' alone.
+template <int CG_, int TN_>
 struct Shape {
-  static constexpr int CG = CG_, TILE = 128 * CG_;
-  static constexpr int COLS = TILE / 2;                 // result columns of an epilogue warp
+  static constexpr int CG = CG_, TM = 128 * CG_, TN = TN_;
+  static constexpr int BN = TN / CG;                    // columns of B that a CTA loads
+  static constexpr int EPI = TN >= 128 ? kEpiWarps : 4; // epilogue warps
+  static constexpr int COLS = TN * 4 / EPI;             // result columns of each
 };
-constexpr int kOperand = 128 * BK * 2;     // bytes of a CTA's rows of A, and of its columns of B
+constexpr int kOperand = 128 * BK * 2;     // bytes of a CTA's rows of A, and at most of its columns of B
 // (three stages are enough while X fits L2, and cost 15 % where it does not)
 constexpr int STAGES = 5;
 constexpr size_t kSmem = (size_t)STAGES * 2 * kOperand + kEpiWarps * kEpiStage + 1024 + 512;
@@ -89,10 +92,10 @@ struct Job {
   float fa[kMaxSteps], da[kMaxSteps];  // square: + fa A + da I
 };
 struct Maps {
-  CUtensorMap xk[2], xn[2];   // X: operand read K-major, right operand read N-major,
+  CUtensorMap xk[2], xr[2], xn[2];   // X: left operand, right operand read K- and N-major,
   CUtensorMap xs[2], xm[2];   //    pieces as computed and mirrored
-  CUtensorMap ak, as, am;     // A: operand, pieces
-  CUtensorMap bk, bs, bm;     // B: operand, pieces
+  CUtensorMap ak, ar, as, am; // A: left and right operand, pieces
+  CUtensorMap bk, bs, bm;     // B: left operand, pieces
 };
 
 struct Work {
@@ -162,10 +165,10 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, 
       : "memory");
 }
 
-// kind::f16, fp16 operands, fp32 accumulator, TILE x TILE; bit 16: B is N-major
+// kind::f16, fp16 operands, fp32 accumulator, TM x TN tile; bit 16: B is N-major
 template <typename S>
 __device__ __forceinline__ constexpr uint32_t idesc() {
-  return (1u << 4) | ((uint32_t)(S::TILE >> 3) << 17) | ((uint32_t)(S::TILE >> 4) << 24);
+  return (1u << 4) | ((uint32_t)(S::TN >> 3) << 17) | ((uint32_t)(S::TM >> 4) << 24);
 }
 
 // until *cnt >= target
@@ -360,8 +363,8 @@ __device__ __forceinline__ void emit_user(const Job& p, const float* v, float f,
 template <typename S>
 __global__ void __launch_bounds__(kThreads, 1)
 ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
-  constexpr int CG = S::CG, TILE = S::TILE;
-  constexpr uint32_t TMEM_COLS = 2 * TILE;
+  constexpr int CG = S::CG, TN = S::TN;
+  constexpr uint32_t TMEM_COLS = 2 * TN;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -395,13 +398,13 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_u32(tfull + a), 1);
-      mbar_init(smem_u32(tempty + a), kEpiWarps * CG);
+      mbar_init(smem_u32(tempty + a), S::EPI * CG);
     }
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(smem_u32(wfull + s), 1);
       mbar_init(smem_u32(wready + s), 1);
       // the MMA lane, the other CTA's producer, every epilogue warp
-      mbar_init(smem_u32(wempty + s), CG + kEpiWarps * CG);
+      mbar_init(smem_u32(wempty + s), CG + S::EPI * CG);
     }
     for (int i = 0; i < kEpiWarps; ++i) mbar_init(smem_u32(aload + i), 1);
     mbar_init(smem_u32(drain), 1);
@@ -489,7 +492,7 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
         if (before > 0) {
           // the product before this one is complete for this matrix; then order the loads of the
           // asynchronous proxy behind that
-          if (lane == 0) ok = wait_done(job.done + w.g, before * kEpiWarps * CG, ctl);
+          if (lane == 0) ok = wait_done(job.done + w.g, before * S::EPI * CG, ctl);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           __syncwarp();
           asm volatile("fence.proxy.async.global;" ::: "memory");
@@ -499,8 +502,8 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
         const CUtensorMap* ma =
             w.kind == kGram ? &maps.xk[x] : w.kind == kSquare ? &maps.ak : &maps.bk;
         const CUtensorMap* mb =
-            w.kind == kGram ? &maps.xk[x] : w.kind == kSquare ? &maps.ak : &maps.xn[x];
-        const int am = w.mb * TILE + (int)rank * 128, bn = w.nb * TILE + (int)rank * 128;
+            w.kind == kGram ? &maps.xr[x] : w.kind == kSquare ? &maps.ar : &maps.xn[x];
+        const int am = w.mb * S::TM + (int)rank * 128, bn = w.nb * TN + (int)rank * S::BN;
         const int ns = segments(job, w);
         for (int seg = 0; ok && seg < ns; ++seg) {
           const int za = part_a(ns, seg) * job.batch + w.g, zb = part_b(ns, seg) * job.batch + w.g;
@@ -514,11 +517,11 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
             const uint32_t da = smem_u32(sa) + (uint32_t)(s * kOperand);
             const uint32_t db = smem_u32(sb) + (uint32_t)(s * kOperand);
             if (elect_one()) {
-              if (leader) mbar_expect_tx(smem_u32(full + s), CG * 2 * kOperand);
+              if (leader) mbar_expect_tx(smem_u32(full + s), CG * (kOperand + S::BN * BK * 2));
               load_box<CG>(da, ma, fb, kk, am, za);
               if (w.kind == kUpdate) {
                 load_box<CG>(db, mb, fb, bn, kk, zb);
-                load_box<CG>(db + 64 * BK * 2, mb, fb, bn + 64, kk, zb);
+                if constexpr (S::BN == 128) load_box<CG>(db + 64 * BK * 2, mb, fb, bn + 64, kk, zb);
               } else {
                 load_box<CG>(db, mb, fb, kk, bn, zb);
               }
@@ -559,7 +562,7 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
             ok = wait_inline(smem_u32(tempty + acc), ((uint32_t)(count >> 1) & 1u) ^ 1u, ctl, kErrMma);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after();
-            const uint32_t d = tmem_base + (uint32_t)(acc * TILE);
+            const uint32_t d = tmem_base + (uint32_t)(acc * TN);
             for (uint32_t more = 0u; kb < end; ++kb, more = 1u) {
               ok = wait_inline(smem_u32(full + s), ph, ctl, kErrMma);
               if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -596,14 +599,14 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
     uint32_t aphase = 0;
     int count = 0;
     bool ok = true, loading = false;   // (a tile of A is on its way into the stage)
-    for (int n = 0; ok; ++n) {
+    for (int n = 0; ok && warp - 4 < S::EPI; ++n) {
       int tile;
       if (!take(n, tile) || tile >= job.total) break;
       const Work w = decode(job, tile);
       const Kind& k = job.k[w.kind];
       const int ns = segments(job, w), nk = ns * k.nk, head = head_blocks(job, ns, k.nk);
-      const int row0 = w.mb * TILE + (int)rank * 128 + quarter * 32;
-      const int base0 = w.nb * TILE + cbase;
+      const int row0 = w.mb * S::TM + (int)rank * 128 + quarter * 32;
+      const int base0 = w.nb * TN + cbase;
       // A's 64 columns from c on, for b A, into the stage (which the warp has finished with)
       auto load_a = [&](int c) {
         if (lane == 0) {
@@ -632,7 +635,7 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
         const uint32_t trow = tmem_base + ((uint32_t)(quarter * 32) << 16) +
-                              (uint32_t)(acc * TILE + cbase);
+                              (uint32_t)(acc * TN + cbase);
 #pragma unroll
         for (int c = 0; c < COLS; c += 32) {
           uint32_t r[32];
@@ -961,10 +964,10 @@ int sm_total() {
   return n > 0 ? n : 148;
 }
 
-Kind kind_of(int64_t rows, int64_t cols, int64_t K, int tile, bool sym) {
+Kind kind_of(int64_t rows, int64_t cols, int64_t K, int tm, int tn, bool sym) {
   Kind k;
-  k.tiles_m = (int)((rows + tile - 1) / tile);
-  k.tiles_n = (int)((cols + tile - 1) / tile);
+  k.tiles_m = (int)((rows + tm - 1) / tm);
+  k.tiles_n = (int)((cols + tn - 1) / tn);
   k.sym = sym;
   k.cols = (int)cols;
   k.nk = (int)(K / BK);
@@ -972,35 +975,37 @@ Kind kind_of(int64_t rows, int64_t cols, int64_t K, int tile, bool sym) {
   return k;
 }
 
-// Tile shape (CTAs that share a tile) and use of symmetry of a problem.
+// Tile shape and use of symmetry of a problem.
 struct Choice {
-  int cg;
+  int cg, tn;
   bool sym;
 };
-// The fastest of three by a model of one step: the work of all matrices shared out over the GPU, and
+// The fastest of four by a model of one step: the work of all matrices shared out over the GPU, and
 // one matrix's three products one after the other, each in whole waves of tiles; the longer of the
-// two and a third of the other. Its figures (us) are a fit to 54 problems of 1 to 100 matrices of
-// 192 to 4096 rows: the choice takes at most 6 % more than the best of the three. Where symmetry or
-// the large tile pays, and where it does not (256 x 256 symmetric, 128 x 128 symmetric, 128 x 128
-// full, us in one run): 4096 x 4096 bf16 1643, 2138, 2687; 36 blocks of 512 499, 464, 668;
-// 4096 x 1024 bf16 314, 265, 259; 3 of 1000 x 333 fp32 282, 214, 199. Never the fastest, and so not
-// here: 256 x 256 full (2113, 534, 305, 282); 256 x 128 tiles of a pair (at most 3 % ahead of
-// 128 x 128: 4096 x 1024 fp32 544, 551).
+// two and a third of the other. Its figures (us) are a fit to 57 problems of 1 to 100 matrices of
+// 60 to 4096 rows: the choice takes at most 9 % more than the best of the four, runs of one choice
+// differing by half of that. Where each pays (256 x 256 symmetric, 128 x 128 symmetric, 128 x 128
+// full, 128 x 64, us in one run): 4096 x 4096 bf16 1462, 1990, 2678, 4633; 100 blocks of 256 355, 307,
+// 368, 516; 4096 x 1024 bf16 313, 260, 256, 310; 3 of 1000 x 333 fp32 306, 230, 215, 199. Never the
+// fastest, and so not here: 256 x 256 full (36 blocks of 512 534, of 128 x 128 symmetric 464); 256 x
+// 128 tiles of a pair (at most 3 % ahead of 128 x 128).
 Choice choose(const Problem& p, const Dims& d, int sms) {
   const bool exact = p.out_t == DT::F32, skew = p.form == Form::Skew;
-  if (d.R <= 128) return {1, false};   // one row of tiles: nothing to mirror
   Choice best{};
   double best_t = 1e30;
-  for (const Choice c : {Choice{2, true}, Choice{1, true}, Choice{1, false}}) {
-    const int tile = 128 * c.cg, workers = sms / c.cg;
+  for (const Choice c : {Choice{2, 256, true}, Choice{1, 128, true}, Choice{1, 128, false},
+                         Choice{1, 64, false}}) {
+    if (c.sym && d.R <= 128) continue;   // one row of tiles: nothing to mirror
+    const int tm = 128 * c.cg, workers = sms / c.cg;
     // a K block with every SM busy and in a chain; a tile's way out per part, and what a product
     // takes besides from its last store to the next one's first load
-    const double busy_us = c.cg == 2 ? 0.47 : 0.33, block_us = c.cg == 2 ? 0.28 : 0.17;
+    const double busy_us = c.cg == 2 ? 0.47 : c.tn == 128 ? 0.33 : 0.25;
+    const double block_us = c.cg == 2 ? 0.28 : c.tn == 128 ? 0.17 : 0.11;
     const double part_us = c.cg == 2 ? 3.6 : 2.6, gap_us = c.cg == 2 ? 4.0 : 2.2;
     double work = 0.0, chain = 0.0;
     for (int kind = 0; kind < 3; ++kind) {
       const bool sym = c.sym && (kind < 2 || skew);
-      const Kind k = kind_of(d.R, kind < 2 ? d.R : d.ld, kind == 0 ? d.ld : d.R, tile, sym);
+      const Kind k = kind_of(d.R, kind < 2 ? d.R : d.ld, kind == 0 ? d.ld : d.R, tm, c.tn, sym);
       const int blocks = k.nk * (exact ? 3 : kind == 2 ? 2 : 1);
       const double out =
           part_us * (exact || kind == 2 ? 2 : 1) * (sym && k.per > 1 ? 1.25 : 1.0);
@@ -1150,7 +1155,7 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
   }
   const int sms = sm_total();
   const Choice c = choose(p, d, sms);
-  const int tile = 128 * c.cg;
+  const int tm = 128 * c.cg, bn = c.tn / c.cg;
 
   Maps maps{};
   const int64_t mats = 2 * p.batch;
@@ -1159,11 +1164,13 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
   for (int i = 0; i < 2; ++i) {
     if (!w.x[i]) continue;
     ok = ok && make_map3(&maps.xk[i], w.x[i], mats, d.R, d.ld, 64, 128, k128) &&
+         make_map3(&maps.xr[i], w.x[i], mats, d.R, d.ld, 64, bn, k128) &&
          make_map3(&maps.xn[i], w.x[i], mats, d.R, d.ld, 64, 64, k128) &&
          make_map3(&maps.xs[i], w.x[i], mats, d.R, d.ld, 64, 32, k128) &&
          make_map3(&maps.xm[i], w.x[i], mats, d.R, d.ld, 32, 64, k64);
   }
   ok = ok && make_map3(&maps.ak, w.a, mats, d.R, d.R, 64, 128, k128) &&
+       make_map3(&maps.ar, w.a, mats, d.R, d.R, 64, bn, k128) &&
        make_map3(&maps.as, w.a, mats, d.R, d.R, 64, 32, k128) &&
        make_map3(&maps.am, w.a, mats, d.R, d.R, 32, 64, k64) &&
        make_map3(&maps.bk, w.b, mats, d.R, d.R, 64, 128, k128) &&
@@ -1172,15 +1179,16 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
   if (!ok) return cudaErrorInvalidValue;
 
   Job job{};
-  job.k[kGram] = kind_of(d.R, d.R, d.ld, tile, c.sym);
-  job.k[kSquare] = kind_of(d.R, d.R, d.R, tile, c.sym);
-  job.k[kUpdate] = kind_of(d.R, d.ld, d.R, tile, c.sym && skew);
+  job.k[kGram] = kind_of(d.R, d.R, d.ld, tm, c.tn, c.sym);
+  job.k[kSquare] = kind_of(d.R, d.R, d.R, tm, c.tn, c.sym);
+  job.k[kUpdate] = kind_of(d.R, d.ld, d.R, tm, c.tn, c.sym && skew);
   job.batch = (int)p.batch;
   job.steps = p.steps;
   int64_t per_step = 0;
   for (const Kind& k : job.k) per_step += (int64_t)k.per * p.batch;
-  // the counts reach 16 per tile
-  if (per_step * p.steps * 16 > INT32_MAX) return cudaErrorInvalidValue;
+  // a matrix's count rises by one per epilogue warp of a tile
+  if (per_step * p.steps * (c.tn == 64 ? 4 : kEpiWarps * c.cg) > INT32_MAX)
+    return cudaErrorInvalidValue;
   job.per_step = (int)per_step;
   job.total = job.per_step * p.steps;
   job.R = (int)d.R;
@@ -1201,7 +1209,9 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
   job.done = w.counts + 1;
   job.err = err;
   fill_factors(p, plan, job.f, job.fa, job.da);
-  return c.cg == 1 ? launch<Shape<1>>(maps, job, sms, s) : launch<Shape<2>>(maps, job, sms, s);
+  if (c.cg == 2) return launch<Shape<2, 256>>(maps, job, sms, s);
+  return c.tn == 128 ? launch<Shape<1, 128>>(maps, job, sms, s)
+                     : launch<Shape<1, 64>>(maps, job, sms, s);
 }
 
 }  // namespace orth
