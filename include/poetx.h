@@ -349,7 +349,7 @@ poetx_status poetx_orthogonalize_q(const float* u, int64_t nblocks, int64_t b, c
  *     y = (x - mean) rstd gamma + beta.
  *   x [T, m] and y [T, m] have `dtype`; y may be x. gamma, beta [m] have `w_dtype`; NULL stands
  *   for ones and zeros. mean, rstd [T] fp32 outputs for the backward (either may be NULL).
- *   Any T and m <= 2^20 (rows need not be a multiple of anything); sums are fp32, y is rounded
+ *   m <= 2^20, T m <= 2^50 (rows need not be a multiple of anything); sums are fp32, y is rounded
  *   once. A row that holds NaN or infinity gives NaN in that row only; a constant row gives beta
  *   up to rounding (with eps = 0 the formula is 0 / 0 there).
  *   Errors: INVALID_ARG (NULL x or y, negative size, eps negative or not finite), SHAPE, DTYPE,

@@ -947,19 +947,23 @@ poetx_status poetx_merge_reinit(poetx_layer* L, uint64_t seed, void* workspace, 
 // ------------------------------------------------------------------ Newton-Schulz
 namespace {
 
+// Sizes that the products' tile counters hold (sizes and steps are not negative).
+bool orth_fits(int64_t batch, int64_t m, int64_t n, int32_t steps) {
+  return batch <= 65535 && m <= 65536 && n <= 65536 &&
+         batch * ((m + 127) / 128) * ((n + 127) / 128) * 3 * steps <= (int64_t)INT32_MAX / 16;
+}
+
 // One Newton-Schulz problem and its argument checks, shared by the dense and the packed form.
 poetx_status check_orth(const char* what, orth::Problem* p, int64_t batch, int64_t m, int64_t n,
                         const float* coeffs, int32_t steps, float eps, float scale,
                         orth::Plan* plan) {
-  constexpr int64_t kMaxSide = 65536, kMaxBatch = 65535;
   if (batch < 0 || m < 0 || n < 0)
     return fail(POETX_ERR_INVALID_ARG, "%s: negative size", what);
   if (!coeffs) return fail(POETX_ERR_INVALID_ARG, "%s: coeffs is NULL", what);
   if (steps < 1 || steps > POETX_ORTH_MAX_STEPS)
     return fail(POETX_ERR_INVALID_ARG, "%s: steps=%d is not in 1..%d", what, (int)steps,
                 POETX_ORTH_MAX_STEPS);
-  if (batch > kMaxBatch || m > kMaxSide || n > kMaxSide ||
-      batch * ((m + 127) / 128) * ((n + 127) / 128) * 3 * steps > (int64_t)INT32_MAX / 16)
+  if (!orth_fits(batch, m, n, steps))
     return fail(POETX_ERR_SHAPE, "%s: %lld matrices of %lld x %lld exceed the supported sizes", what,
                 (long long)batch, (long long)m, (long long)n);
   if (!(eps >= 0.f) || !std::isfinite(eps) || !std::isfinite(scale))
@@ -988,8 +992,8 @@ poetx_status run_orth(const char* what, const orth::Problem& p, const orth::Plan
 
 // The sizes of a workspace query; false where the call itself would refuse them.
 bool orth_sizes_ok(int64_t batch, int64_t m, int64_t n, int32_t steps) {
-  return batch > 0 && m > 0 && n > 0 && batch <= 65535 && m <= 65536 && n <= 65536 && steps >= 1 &&
-         steps <= POETX_ORTH_MAX_STEPS;
+  return batch > 0 && m > 0 && n > 0 && steps >= 1 && steps <= POETX_ORTH_MAX_STEPS &&
+         orth_fits(batch, m, n, steps);
 }
 
 }  // namespace
@@ -1045,12 +1049,15 @@ poetx_status poetx_orthogonalize_q(const float* u, int64_t nblocks, int64_t b, c
 // ------------------------------------------------------------------ layer norm
 namespace {
 constexpr int64_t kMaxNormWidth = (int64_t)1 << 20;
+constexpr int64_t kMaxNormElems = (int64_t)1 << 50;   // byte offsets stay far inside 64 bits
 
 poetx_status check_norm(const char* what, int64_t T, int64_t m, int32_t dtype, int32_t w_dtype) {
   if (T < 0 || m < 0) return fail(POETX_ERR_INVALID_ARG, "%s: negative size", what);
   if (m > kMaxNormWidth)
     return fail(POETX_ERR_SHAPE, "%s: m=%lld exceeds %lld", what, (long long)m,
                 (long long)kMaxNormWidth);
+  if (m > 0 && T > kMaxNormElems / m)
+    return fail(POETX_ERR_SHAPE, "%s: %lld x %lld elements", what, (long long)T, (long long)m);
   for (int32_t d : {dtype, w_dtype})
     if (d != POETX_F32 && d != POETX_BF16)
       return fail(POETX_ERR_DTYPE, "%s: unknown dtype %d", what, (int)d);

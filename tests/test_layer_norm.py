@@ -342,7 +342,7 @@ def test_inputs_written_by_the_launch_before(m):
     (dict(eps=float("nan")), 1), (dict(eps=float("inf")), 1), (dict(m=(1 << 20) + 1), 2),
     (dict(dt=2), 4), (dict(wd=-1), 4), (dict(x=0x10002), 3), (dict(gamma=0x20004), 3),
     (dict(beta=0x20008), 3), (dict(y=0x30001), 3), (dict(mean=0x40004), 3), (dict(rstd=0x40004), 3),
-    (dict(T=0, x=None, y=None), 0), (dict(m=0), 0),
+    (dict(T=0, x=None, y=None), 0), (dict(m=0), 0), (dict(T=1 << 62, m=4), 2),
 ])
 def test_forward_refusals(kw, status):
     a = dict(x=0x10000, T=4, m=64, dt=0, gamma=0x20000, beta=0x28000, wd=0, eps=1e-5, y=0x30000,
@@ -359,7 +359,7 @@ def test_forward_refusals(kw, status):
     (dict(x=0x10004), 3), (dict(dy=0x18004), 3), (dict(dx=0x30004), 3), (dict(dgamma=0x60004), 3),
     (dict(dbeta=0x60008), 3), (dict(gamma=0x20001), 3), (dict(), 8),
     (dict(ws=0x90000, wsb=4), 8), (dict(ws=0x90004, wsb=1 << 30), 3),
-    (dict(dx=None, dgamma=None, dbeta=None), 0), (dict(m=0), 0),
+    (dict(dx=None, dgamma=None, dbeta=None), 0), (dict(m=0), 0), (dict(T=1 << 49, m=4), 2),
 ])
 def test_backward_refusals(kw, status):
     a = dict(x=0x10000, dy=0x18000, T=4, m=64, dt=0, gamma=0x20000, wd=0, mean=0x40000,

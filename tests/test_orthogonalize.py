@@ -395,6 +395,7 @@ def test_workspace_alignment_and_empty_calls():
     assert poetx.lib.poetx_orthogonalize_workspace_bytes(1, 0, 64, 1) == 0
     assert poetx.lib.poetx_orthogonalize_workspace_bytes(1, 64, 64, 0) == 0
     assert poetx.lib.poetx_orthogonalize_workspace_bytes(-1, 64, 64, 5) == 0
+    assert poetx.lib.poetx_orthogonalize_workspace_bytes(65535, 65536, 65536, 5) == 0
 
 
 @pytest.mark.parametrize("kw,status", [
