@@ -25,16 +25,20 @@
 // the host from the range of the singular values after each step (X_0 has them in [0, 1]; the
 // quintic's range over an interval is known), so nothing overflows and the smallest entries that
 // matter stay normal numbers.
-//   fp32 results: every product is hi hi + hi lo + lo hi (three passes over K), error a few
-//     2^-22 of the result's size.
-//   bf16 results: one pass for gram and square; the update of every step but the last reads X in
-//     both parts (two passes). X's rounding is what the iteration amplifies: a direction whose
+//   fp32 results, and bf16 results of up to 128 rows: every product is hi hi + hi lo + lo hi (three
+//     passes over K), error a few 2^-22 of the result's size.
+//   other bf16 results: one pass for gram and square; the update of every step but the last reads X
+//     in both parts (two passes). X's rounding is what the iteration amplifies: a direction whose
 //     singular value is 1e-3 of the largest is drowned by 2^-11 of the large ones, and it
 //     is lifted by a = 3.4 a step while they stay. The rounding of A, H and B acts on the
 //     directions in proportion and is not amplified. Against the exact result, in units of its
 //     rms: 1.4e-3 for an update of a few strong directions over a background (single-part X
 //     2.0e-3, and 9.5e-3 with a background of 3 % of the strongest); bf16 rounding alone is
-//     1.7e-3.
+//     1.7e-3. That is an average over the directions, each of which one rounding of A or B may
+//     move by up to 7e-3: 1.1e-3 of Gaussian matrices of 128 rows and more, but 1.7e-3 of 64 rows
+//     and 6e-3 of two, and 7e-3 of any size where all singular values coincide. Three passes for
+//     every size would be free of it and take 1.3 (200 x 300) to 2.2 times as long (4096 x 14336 11.0
+//     ms against 5.1 ms); up to 128 rows they take 1.2 to 1.3 times (64 x 300 104 us against 82).
 #include "orth_mma.cuh"
 
 #include <algorithm>
@@ -83,7 +87,7 @@ struct Job {
   Kind k[3];
   int batch, steps, per_step, total;   // tiles per step (all matrices) and in all
   int R;                               // padded rows of every result
-  int exact, chunk;                    // chunk: K blocks per accumulator of an fp32 result
+  int exact, chunk;                    // three part products; then K blocks per accumulator
   int fmode, out_f32, vec;             // the caller's array: layout, type, rows start on 16 bytes
   void* out;
   long long um, un;                    // its rows and columns (of the result as computed)
@@ -135,7 +139,7 @@ __device__ __forceinline__ int segments(const Job& j, const Work& w) {
 __device__ __forceinline__ int part_a(int n, int seg) { return n == 3 && seg == 0; }
 __device__ __forceinline__ int part_b(int n, int seg) { return n > 1 && seg == n - 2; }
 // K blocks that the first accumulator of a tile sums: the small products and the first job.chunk of
-// the large one for fp32 results, everything otherwise
+// the large one with three part products, everything otherwise
 __device__ __forceinline__ int head_blocks(const Job& j, int n, int nk) {
   return j.exact ? (n - 1) * nk + min(j.chunk, nk) : n * nk;
 }
@@ -918,6 +922,11 @@ bool make_map3(CUtensorMap* m, const void* base, int64_t mats, int64_t rows, int
             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Three part products, or fewer where a bf16 result's directions are many.
+bool three_products(const Problem& p) {
+  return p.out_t == DT::F32 || std::min(p.m, p.n) <= 128;
+}
+
 struct Dims {
   int64_t r, k, R, ld;
   bool tall;
@@ -990,7 +999,7 @@ struct Choice {
 // fastest, and so not here: 256 x 256 full (36 blocks of 512 534, of 128 x 128 symmetric 464); 256 x
 // 128 tiles of a pair (at most 3 % ahead of 128 x 128).
 Choice choose(const Problem& p, const Dims& d, int sms) {
-  const bool exact = p.out_t == DT::F32, skew = p.form == Form::Skew;
+  const bool exact = three_products(p), skew = p.form == Form::Skew;
   Choice best{};
   double best_t = 1e30;
   for (const Choice c : {Choice{2, 256, true}, Choice{1, 128, true}, Choice{1, 128, false},
@@ -1126,7 +1135,7 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
   int* err = device_error_word();
   if (!err) return cudaErrorUnknown;
   const bool skew = p.form == Form::Skew;
-  const bool exact = p.out_t == DT::F32;
+  const bool exact = three_products(p), out_f32 = p.out_t == DT::F32;
   const int in_f32 = p.in_t == DT::F32;
   {
     TraceScope t("ns_norm", s);
@@ -1201,10 +1210,10 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
   job.chunk = d.R <= 512 ? 1 : 2;
   job.fmode = skew ? kPacked : d.tall ? kTransposed : kRows;
   job.out = out;
-  job.out_f32 = exact;
+  job.out_f32 = out_f32;
   job.um = d.r;
   job.un = d.k;
-  job.vec = (d.k * (exact ? 4 : 2)) % 16 == 0;
+  job.vec = (d.k * (out_f32 ? 4 : 2)) % 16 == 0;
   job.counter = w.counts;
   job.done = w.counts + 1;
   job.err = err;

@@ -1,8 +1,9 @@
 // Newton-Schulz orthogonalisation of small matrices (at most 128 x 128, packed blocks up to 128):
 // one CTA per matrix and one launch for everything. X, A and B stay in shared memory as fp16 parts
 // in the tensor core's operand layouts, accumulators in tensor memory; the formulas, scales, part
-// products and their order are those of orth.cu, whose fifteen dependent products cost about 6 us
-// each in round trips through L2 (100 us for 16 blocks of 64; here 28 us, the time of one matrix).
+// products (three, for bf16 results too) and their order are those of orth.cu, whose fifteen dependent
+// products cost about 6 us each in round trips through L2 (100 us for 16 blocks of 64; here 28 us, the
+// time of one matrix).
 //
 // An operand is 128 rows x 128 columns per part: two chunks of 64 columns, 128 rows of 128 bytes
 // each, 16-byte unit u of row i at u ^ (i & 7). As a left or right operand of gram and square, and
@@ -20,11 +21,11 @@ constexpr int kThreads = kNormThreads;               // eight warps
 constexpr uint32_t kChunkBytes = 128 * 128;          // 128 rows x 64 columns
 constexpr uint32_t kPartBytes = 2 * kChunkBytes;     // one part of one operand
 constexpr uint32_t kOperandBytes = 2 * kPartBytes;
-// For fp32 results the large product is summed in several accumulators, four of 16 of K = 64 or two of
-// 64 of K = 128, and those are added in registers: the tensor core truncates what it adds (see
-// ns_kernel in orth.cu). Blocks of 32, 64, 128: 1.3, 0.8, 1.1 times the error of fp32 products; with
-// one accumulator 1.5, 1.4, 1.7 times in 3 to 10 % less time (16 blocks of 64 27.1 us against 28.0,
-// 3 of 128 42.6 us against 47.3).
+// The large product is summed in several accumulators, four of 16 of K = 64 or two of 64 of K = 128,
+// and those are added in registers: the tensor core truncates what it adds (see ns_kernel in orth.cu).
+// Blocks of 32, 64, 128: 1.3, 0.8, 1.1 times the error of fp32 products; with one accumulator 1.5,
+// 1.4, 1.7 times in 3 to 10 % less time (16 blocks of 64 27.1 us against 28.0, 3 of 128 42.6 us
+// against 47.3).
 constexpr int kMostAccs = 4;
 constexpr uint32_t kTmemCols = kSmallSide * kMostAccs;
 constexpr int kOutLd = kSmallSide + 1;               // staged results: floats per row
@@ -35,7 +36,7 @@ static_assert((size_t)kSmallSide * kOutLd * sizeof(float) <= 2 * kOperandBytes,
 struct Small {
   const void* x;
   void* out;
-  int in_f32, out_f32, skew, tall, steps, exact, fmode;
+  int in_f32, out_f32, skew, tall, steps, fmode;
   int m, n, r, k;                      // the caller's matrix; as worked on, r <= k
   long long elems;                     // values of one matrix in the caller's arrays
   double eps, sx;
@@ -151,26 +152,23 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
   bool ok = true;
   for (int q = 0; ok && q < 3 * p.steps; ++q) {
     const int t = q / 3, kind = q - 3 * t;
-    const bool last = t + 1 == p.steps, out = kind == kUpdate && last;
+    const bool out = kind == kUpdate && t + 1 == p.steps;
     const int N = kind == kUpdate ? ld : R, K = kind == kGram ? ld : R;
     if (warp == 0) {
-      const int ns = p.exact ? 3 : kind == kUpdate && !last ? 2 : 1;
       const int deep = K == 64 ? 4 : 6;   // 16 or 64 of K an accumulator
       const uint32_t id = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24) |
                           (kind == kUpdate ? 1u << 16 : 0u);
       const uint32_t sa = smem_u32(kind == kGram ? X : kind == kSquare ? A : B);
       const uint32_t sb = smem_u32(kind == kSquare ? A : X);
-      for (int seg = 0; seg < ns; ++seg) {
-        // hi hi | hi lo, hi hi | lo hi, hi lo, hi hi
-        const uint32_t pa = ns == 3 && seg == 0 ? kPartBytes : 0u;
-        const uint32_t pb = ns > 1 && seg == ns - 2 ? kPartBytes : 0u;
+      for (int seg = 0; seg < 3; ++seg) {   // lo hi, hi lo, hi hi
+        const uint32_t pa = seg == 0 ? kPartBytes : 0u, pb = seg == 1 ? kPartBytes : 0u;
         for (int k = 0; k < K; k += 16) {
           const uint32_t kmaj = (uint32_t)(k >> 6) * kChunkBytes + (uint32_t)(k & 63) * 2;
           const uint32_t a = desc_lo(sa + pa + kmaj, 16);
           const uint32_t b = kind == kUpdate ? desc_lo(sb + pb + (uint32_t)k * 128, kChunkBytes)
                                              : desc_lo(sb + pb + kmaj, 16);
           // the small products and the first part of the large one share an accumulator
-          const int acc = p.exact && seg == ns - 1 ? k >> deep : 0;
+          const int acc = seg == 2 ? k >> deep : 0;
           const bool more = acc > 0 ? (k & ((1 << deep) - 1)) > 0 : seg > 0 || k > 0;
           if (elect_one())
             mma<1>(tmem + (uint32_t)(acc * kSmallSide), a, b, id, more ? 1u : 0u);
@@ -189,22 +187,20 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
       float v[32];
       {
         uint32_t r[kMostAccs][32];
-        const int accs = !p.exact ? 1 : K == 64 ? 4 : 2;
+        const bool four = K == 64;
         tmem_ld32_start(trow + (uint32_t)c0, r[0]);
-        if (accs > 1) tmem_ld32_start(trow + (uint32_t)(kSmallSide + c0), r[1]);
-        if (accs > 2) {
+        tmem_ld32_start(trow + (uint32_t)(kSmallSide + c0), r[1]);
+        if (four) {
           tmem_ld32_start(trow + (uint32_t)(2 * kSmallSide + c0), r[2]);
           tmem_ld32_start(trow + (uint32_t)(3 * kSmallSide + c0), r[3]);
         }
         tmem_arrived(r[0]);
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[0][i]);
-        if (accs > 1) {
-          tmem_arrived(r[1]);
+        tmem_arrived(r[1]);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(r[1][i]);
-        }
-        if (accs > 2) {
+        for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(r[1][i]);
+        if (four) {
           tmem_arrived(r[2]);
           tmem_arrived(r[3]);
 #pragma unroll
@@ -232,8 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 a2 = __half22float2(*reinterpret_cast<const __half2*>(&hw[i]));
-            const float2 b2 = p.exact ? __half22float2(*reinterpret_cast<const __half2*>(&lw[i]))
-                                      : make_float2(0.f, 0.f);
+            const float2 b2 = __half22float2(*reinterpret_cast<const __half2*>(&lw[i]));
             e[2 * i] += (a2.x + b2.x) * fa;
             e[2 * i + 1] += (a2.y + b2.y) * fa;
           }
@@ -293,7 +288,7 @@ cudaError_t run_small(const Problem& p, const Plan& plan, const void* x, void* o
   q.x = x;
   q.out = out;
   q.in_f32 = p.in_t == DT::F32;
-  q.exact = q.out_f32 = p.out_t == DT::F32;
+  q.out_f32 = p.out_t == DT::F32;
   q.skew = p.form == Form::Skew;
   q.tall = !q.skew && p.m > p.n;
   q.fmode = q.skew ? kPacked : kRows;
