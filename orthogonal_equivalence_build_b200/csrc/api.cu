@@ -968,11 +968,11 @@ poetx_status check_orth(const char* what, orth::Problem* p, int64_t batch, int64
                 (long long)batch, (long long)m, (long long)n);
   if (!(eps >= 0.f) || !std::isfinite(eps) || !std::isfinite(scale))
     return fail(POETX_ERR_INVALID_ARG, "%s: eps must be finite and >= 0, scale finite", what);
-  if (!orth::make_plan(coeffs, steps, plan))
-    return fail(POETX_ERR_INVALID_ARG,
-                "%s: coefficients not finite, or the singular values pass 1e6 under them", what);
   p->batch = batch; p->m = m; p->n = n;
   p->steps = steps; p->coeffs = coeffs; p->eps = eps; p->scale = scale;
+  if (!orth::make_plan(*p, plan))
+    return fail(POETX_ERR_INVALID_ARG,
+                "%s: coefficients not finite, or the singular values pass 1e6 under them", what);
   return POETX_OK;
 }
 

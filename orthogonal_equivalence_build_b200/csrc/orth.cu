@@ -92,8 +92,7 @@ struct Job {
   void* out;
   long long um, un;                    // its rows and columns (of the result as computed)
   int *counter, *done, *err;           // tiles handed out; per matrix: epilogue warps finished
-  float f[3][kMaxSteps];               // result = acc f
-  float fa[kMaxSteps], da[kMaxSteps];  // square: + fa A + da I
+  Factors step[kMaxSteps];
 };
 struct Maps {
   CUtensorMap xk[2], xr[2], xn[2];   // X: left operand, right operand read K- and N-major,
@@ -656,7 +655,7 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
       }
       if (!ok) break;
       const bool out = w.kind == kUpdate && w.last;
-      const float f = job.f[w.kind][w.t];
+      const float f = job.step[w.t].f[w.kind];
       if (out) {
 #pragma unroll
         for (int c = 0; c < COLS; c += 64) {
@@ -669,7 +668,7 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
       }
       if (w.kind == kSquare) {
         // v <- v f + A fa
-        const float fa = job.fa[w.t];
+        const float fa = job.step[w.t].fa;
 #pragma unroll
         for (int c = 0; c < COLS; c += 64) {
           if (c > 0) load_a(c);
@@ -710,7 +709,7 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
         const int col0 = base0 + c;   // pieces wholly in the padding are not stored
         if (row0 < job.R && col0 < k.cols)
           emit_maps(to, to_mirror, v + c, w.kind == kSquare ? 1.f : f,
-                    w.kind == kSquare ? job.da[w.t] : 0.f, parts, job.batch, w.g, row0, col0,
+                    w.kind == kSquare ? job.step[w.t].da : 0.f, parts, job.batch, w.g, row0, col0,
                     mirror, w.kind == kUpdate ? 0x80008000u : 0u, smem_u32(stage), lane);
       }
       // publish: this warp's copies are complete, then the matrix's count goes up
@@ -1062,18 +1061,21 @@ cudaError_t launch(const Maps& maps, const Job& job, int sms, cudaStream_t s) {
 
 // ------------------------------------------------------------------ scales
 namespace {
-constexpr double kTop = 32768.0;   // largest scaled magnitude, half of fp16's range
-// the power of two that brings values of at most `most` to at most kTop
-float pow2_scale(double most) {
-  const int e = (int)std::floor(std::log2(kTop / std::max(most, 1e-30)));
-  return (float)std::ldexp(1.0, std::max(-100, std::min(15, e)));
+// The exponent of the power of two that brings values of at most `most` to between half of fp16's
+// range, 32768, and a half of that. (Nothing but zeros: any.)
+int scale_exponent(double most) {
+  if (!(most > 0.0)) return 0;
+  int k;
+  return std::frexp(most, &k) == 0.5 ? 16 - k : 15 - k;
 }
 }  // namespace
 
-bool make_plan(const float* coeffs, int steps, Plan* plan) {
+bool make_plan(const Problem& p, Plan* plan) {
   double top = 1.0;   // the singular values of X lie in [0, top]
-  for (int t = 0; t < steps; ++t) {
-    const double a = coeffs[3 * t], b = coeffs[3 * t + 1], c = coeffs[3 * t + 2];
+  int ex = scale_exponent(1.02 * top);
+  plan->x0 = ex;
+  for (int t = 0; t < p.steps; ++t) {
+    const double a = p.coeffs[3 * t], b = p.coeffs[3 * t + 1], c = p.coeffs[3 * t + 2];
     if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
     // With l = s^2: B's eigenvalues a + b l + c l^2 and the next singular values
     // s |a + b l + c l^2| over l in [0, top^2] have their extremes at the ends or where the
@@ -1097,29 +1099,24 @@ bool make_plan(const float* coeffs, int steps, Plan* plan) {
     } else if (b != 0.0) {
       look(-a / (3.0 * b));
     }
-    // entries of a matrix do not pass its spectral norm; 2 % for the rounding on the way
-    plan->sx[t] = pow2_scale(1.02 * top);
-    plan->sa[t] = pow2_scale(1.02 * end);
-    plan->sb[t] = pow2_scale(1.02 * bb);
+    // Entries of a matrix do not pass its spectral norm; 2 % for the rounding on the way. The scales
+    // follow the singular values down as well as up: fp16's smallest numbers would cut off the
+    // parts of what shrinks. The factors stay near 2^-15 all the same, since a polynomial's
+    // coefficients are bounded by its largest value; terms that vanish in fp32 vanish beside the others.
     top = 1.02 * x;
+    const int ea = scale_exponent(1.02 * end), eb = scale_exponent(1.02 * bb);
+    const int next = scale_exponent(1.02 * top);
+    Factors& o = plan->step[t];
+    o.f[0] = (float)std::ldexp(1.0, ea - 2 * ex);
+    o.f[1] = (float)std::ldexp(c, eb - 2 * ea);
+    o.fa = (float)std::ldexp(b, eb - ea);
+    o.da = (float)std::ldexp(a, eb);
+    o.f[2] = (float)(t + 1 < p.steps ? std::ldexp(1.0, next - eb - ex)
+                                     : std::ldexp((double)p.scale, -eb - ex));
+    ex = next;
     if (!(top < 1e6) || !(bb < 1e12)) return false;
   }
-  plan->sx[steps] = 1.f;
   return true;
-}
-
-void fill_factors(const Problem& p, const Plan& plan, float (*f)[kMaxSteps], float* fa, float* da) {
-  for (int t = 0; t < p.steps; ++t) {
-    // stored: X sx, A sa, B sb
-    const float* q = p.coeffs + 3 * t;
-    const double sx = plan.sx[t], sa = plan.sa[t], sb = plan.sb[t];
-    const double next = t + 1 < p.steps ? plan.sx[t + 1] : p.scale;
-    f[0][t] = (float)(sa / (sx * sx));
-    f[1][t] = (float)(sb * q[2] / (sa * sa));
-    fa[t] = (float)(sb * q[1] / sa);
-    da[t] = (float)(sb * q[0]);
-    f[2][t] = (float)(next / (sb * sx));
-  }
 }
 
 size_t workspace_bytes(const Problem& p) {
@@ -1153,7 +1150,7 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
     q.vec = !skew && !d.tall && p.n * (in_f32 ? 4 : 2) % 16 == 0;
     q.m = p.m; q.n = p.n;
     q.r = (int)d.r; q.k = (int)d.k; q.R = (int)d.R; q.ld = (int)d.ld;
-    q.eps = p.eps; q.sx = plan.sx[0]; q.norm_mult = skew ? 2.0 : 1.0;
+    q.eps = p.eps; q.sx = std::ldexp(1.0, plan.x0); q.norm_mult = skew ? 2.0 : 1.0;
     q.partial = w.partial; q.out = w.x[0];
     // few blocks per matrix when there are many, each summing the norm's partials once
     const int64_t blocks = std::min<int64_t>(q.tiles, std::max<int64_t>(8, 148 * 8 / p.batch));
@@ -1217,7 +1214,7 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
   job.counter = w.counts;
   job.done = w.counts + 1;
   job.err = err;
-  fill_factors(p, plan, job.f, job.fa, job.da);
+  std::copy(plan.step, plan.step + p.steps, job.step);
   if (c.cg == 2) return launch<Shape<2, 256>>(maps, job, sms, s);
   return c.tn == 128 ? launch<Shape<1, 128>>(maps, job, sms, s)
                      : launch<Shape<1, 64>>(maps, job, sms, s);

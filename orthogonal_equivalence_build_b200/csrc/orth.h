@@ -22,17 +22,18 @@ struct Problem {
   float eps = 0.f, scale = 1.f;
 };
 
+// How the epilogues of one step scale their accumulators: gram, square and update results are f[0..2]
+// times the accumulator, square adds fa A + da I (operands as stored, scales included).
+struct Factors {
+  float f[3], fa, da;
+};
 // Powers of two that hold every operand of every step inside fp16 (see orth.cu).
 struct Plan {
-  float sx[kMaxSteps + 1];   // scale of X before step t
-  float sa[kMaxSteps], sb[kMaxSteps];   // of A and B
+  int x0;                  // X_0 is stored times 2^x0
+  Factors step[kMaxSteps];
 };
 // false: the coefficients are not finite or let the singular values grow past every bound
-bool make_plan(const float* coeffs, int steps, Plan* plan);
-
-// Factors of the epilogues: gram, square and update results are f[0..2][t] times the accumulator;
-// square adds fa[t] A and da[t] I (operands as stored, scales included).
-void fill_factors(const Problem& p, const Plan& plan, float (*f)[kMaxSteps], float* fa, float* da);
+bool make_plan(const Problem& p, Plan* plan);
 
 // One CTA per matrix (orth_small.cu), where a matrix fits into shared memory.
 bool small_fits(const Problem& p);

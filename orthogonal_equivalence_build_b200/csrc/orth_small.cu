@@ -11,6 +11,7 @@
 #include "orth_mma.cuh"
 
 #include <algorithm>
+#include <cmath>
 
 namespace poetx {
 namespace orth {
@@ -41,7 +42,7 @@ struct Small {
   long long elems;                     // values of one matrix in the caller's arrays
   double eps, sx;
   int* err;
-  float f[3][kMaxSteps], fa[kMaxSteps], da[kMaxSteps];   // as in orth.cu
+  Factors step[kMaxSteps];
 };
 
 __device__ __forceinline__ uint32_t at16(int i, int j) {   // byte of element (i, j) in a part
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
     if (!ok) break;
     tc_fence_after();
     // columns past the result's padded width N (64 or 128) are not computed
-    const float f = p.f[kind][t], fa = p.fa[t], da = p.da[t];
+    const float f = p.step[t].f[kind], fa = p.step[t].fa, da = p.step[t].da;
     for (int c0 = half * (N / 2); c0 < (half + 1) * (N / 2); c0 += 32) {
       float v[32];
       {
@@ -299,10 +300,10 @@ cudaError_t run_small(const Problem& p, const Plan& plan, const void* x, void* o
   q.k = (int)std::max(p.m, p.n);
   q.elems = q.skew ? p.m * (p.m - 1) / 2 : p.m * p.n;
   q.eps = p.eps;
-  q.sx = plan.sx[0];
+  q.sx = std::ldexp(1.0, plan.x0);
   q.err = device_error_word();
   if (!q.err) return cudaErrorUnknown;
-  fill_factors(p, plan, q.f, q.fa, q.da);
+  std::copy(plan.step, plan.step + p.steps, q.step);
   cudaError_t e = cudaFuncSetAttribute(ns_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)kSmem);
   if (e != cudaSuccess) return e;

@@ -84,3 +84,28 @@ def test_bf16_results_of_coinciding_singular_values_round_once():
         x = torch.eye(r, 140, device="cuda")[None]
         check_three(run(x, torch.bfloat16), exact(x, [MUON] * 5))
         check_three(run(x[:, :, :r].contiguous(), torch.bfloat16), exact(x[:, :, :r], [MUON] * 5))
+
+
+# ------------------------------------------------------------------ schedules that shrink and grow
+# Linear steps only scale X, so the limits hold however small it gets; (0, b, 0) cubes the singular
+# values and then B = b A alone carries the result.
+@gpu
+@pytest.mark.parametrize("shape", [(2, 200, 300), (3, 60, 100), (2, 320, 150)])
+@pytest.mark.parametrize("coeffs", [
+    [(0.01, 0.0, 0.0)] * 4, [(0.001, 0.0, 0.0)] * 4,
+    [(0.001, 0.0, 0.0)] * 4 + [(1000.0, 0.0, 0.0)] * 4 + [MUON],
+    [(1e-6, 0.0, 0.0), (1e5, 0.0, 0.0), (0.3, -0.2, 0.1)], [(0.0, 0.02, 0.0), (40.0, 0.0, 0.0)],
+    [(0.0, 0.0, 1e-4)], [(1e-4, -3e-4, 1e-4), (0.0, 1e3, 0.0)],
+], ids=range(7))
+def test_schedules_that_shrink_the_singular_values(shape, coeffs):
+    x = gaussian(shape, "f32")
+    check_three(run(x, torch.float32, coeffs), exact(x, coeffs))
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(2, 60, 100), (2, 200, 300)])
+def test_coefficients_of_zero_give_zeros(shape):
+    x = gaussian(shape, "f32")
+    for out_t in (torch.float32, torch.bfloat16):
+        out = run(x, out_t, [MUON, (0.0, 0.0, 0.0), MUON])
+        assert torch.equal(out, torch.zeros_like(out))
