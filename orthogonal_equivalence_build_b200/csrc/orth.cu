@@ -90,6 +90,7 @@ struct Job {
   int exact, chunk;                    // three part products; then K blocks per accumulator
   int fmode, out_f32, vec;             // the caller's array: layout, type, rows start on 16 bytes
   void* out;
+  float out_scale;
   long long um, un;                    // its rows and columns (of the result as computed)
   int *counter, *done, *err;           // tiles handed out; per matrix: epilogue warps finished
   Factors step[kMaxSteps];
@@ -277,7 +278,7 @@ __device__ __forceinline__ void emit_maps(const CUtensorMap* out, const CUtensor
   }
 }
 
-// The same piece to the caller's array.
+// The same piece to the caller's array: v f out_scale.
 __device__ __forceinline__ void emit_user(const Job& p, const float* v, float f, int g, int row0,
                                           int col0, uint8_t* stage, int lane) {
   if (p.fmode == kTransposed) {
@@ -289,12 +290,12 @@ __device__ __forceinline__ void emit_user(const Job& p, const float* v, float f,
         float* o = static_cast<float*>(p.out) + at;
 #pragma unroll
         for (int q = 0; q < 64; ++q, o += p.um)
-          if (q < left) *o = v[q] * f;
+          if (q < left) *o = v[q] * f * p.out_scale;
       } else {
         __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
 #pragma unroll
         for (int q = 0; q < 64; ++q, o += p.um)
-          if (q < left) *o = __float2bfloat16_rn(v[q] * f);
+          if (q < left) *o = __float2bfloat16_rn(v[q] * f * p.out_scale);
       }
     }
     return;
@@ -303,7 +304,8 @@ __device__ __forceinline__ void emit_user(const Job& p, const float* v, float f,
 #pragma unroll
   for (int u = 0; u < 16; ++u)
     *reinterpret_cast<float4*>(stage + lane * 256 + ((u ^ (lane & 15)) << 4)) =
-        make_float4(v[4 * u] * f, v[4 * u + 1] * f, v[4 * u + 2] * f, v[4 * u + 3] * f);
+        make_float4(v[4 * u] * f * p.out_scale, v[4 * u + 1] * f * p.out_scale,
+                    v[4 * u + 2] * f * p.out_scale, v[4 * u + 3] * f * p.out_scale);
   __syncwarp();
   auto unit = [&](int r, int u) {
     return *reinterpret_cast<const float4*>(stage + r * 256 + ((u ^ (r & 15)) << 4));
@@ -1111,8 +1113,11 @@ bool make_plan(const Problem& p, Plan* plan) {
     o.f[1] = (float)std::ldexp(c, eb - 2 * ea);
     o.fa = (float)std::ldexp(b, eb - ea);
     o.da = (float)std::ldexp(a, eb);
-    o.f[2] = (float)(t + 1 < p.steps ? std::ldexp(1.0, next - eb - ex)
-                                     : std::ldexp((double)p.scale, -eb - ex));
+    // The last update takes the operands' scales off and the caller's scale after them: their product
+    // can lie among fp32's smallest numbers where the result does not.
+    const int off = eb + ex, first = std::min(off, 100);
+    o.f[2] = (float)std::ldexp(1.0, t + 1 < p.steps ? next - off : -first);
+    plan->out = (float)std::ldexp((double)p.scale, first - off);
     ex = next;
     if (!(top < 1e6) || !(bb < 1e12)) return false;
   }
@@ -1207,6 +1212,7 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
   job.chunk = d.R <= 512 ? 1 : 2;
   job.fmode = skew ? kPacked : d.tall ? kTransposed : kRows;
   job.out = out;
+  job.out_scale = plan.out;
   job.out_f32 = out_f32;
   job.um = d.r;
   job.un = d.k;

@@ -30,7 +30,8 @@ struct Factors {
 // Powers of two that hold every operand of every step inside fp16 (see orth.cu).
 struct Plan {
   int x0;                  // X_0 is stored times 2^x0
-  Factors step[kMaxSteps];
+  Factors step[kMaxSteps]; // (the last update's f leaves the result itself, or 2^j times it)
+  float out;               // the caller's scale, times 2^-j
 };
 // false: the coefficients are not finite or let the singular values grow past every bound
 bool make_plan(const Problem& p, Plan* plan);

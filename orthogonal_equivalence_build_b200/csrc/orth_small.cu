@@ -41,6 +41,7 @@ struct Small {
   int m, n, r, k;                      // the caller's matrix; as worked on, r <= k
   long long elems;                     // values of one matrix in the caller's arrays
   double eps, sx;
+  float out_scale;
   int* err;
   Factors step[kMaxSteps];
 };
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
       if (out) {
         float* stage = reinterpret_cast<float*>(A);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) stage[row * kOutLd + c0 + c] = v[c];
+        for (int c = 0; c < 32; ++c) stage[row * kOutLd + c0 + c] = v[c] * p.out_scale;
         continue;
       }
       uint8_t* to = kind == kGram ? A : kind == kSquare ? B : X;
@@ -301,6 +302,7 @@ cudaError_t run_small(const Problem& p, const Plan& plan, const void* x, void* o
   q.elems = q.skew ? p.m * (p.m - 1) / 2 : p.m * p.n;
   q.eps = p.eps;
   q.sx = std::ldexp(1.0, plan.x0);
+  q.out_scale = plan.out;
   q.err = device_error_word();
   if (!q.err) return cudaErrorUnknown;
   std::copy(plan.step, plan.step + p.steps, q.step);

@@ -109,3 +109,31 @@ def test_coefficients_of_zero_give_zeros(shape):
     for out_t in (torch.float32, torch.bfloat16):
         out = run(x, out_t, [MUON, (0.0, 0.0, 0.0), MUON])
         assert torch.equal(out, torch.zeros_like(out))
+
+
+# ------------------------------------------------------------------------ the caller's scale
+@gpu
+@pytest.mark.parametrize("shape", [(2, 200, 300), (2, 300, 200), (3, 60, 100)])
+@pytest.mark.parametrize("scale", [1e-36, 1e-34, -1e-30, 1e30, 3e37])
+def test_scales_near_the_ends_of_fp32(shape, scale):
+    x = gaussian(shape, "f32")
+    scale = torch.tensor(scale, dtype=torch.float32).item()
+    check_three(run(x, torch.float32, scale=scale), exact(x, [MUON] * 5, scale=scale))
+    if min(shape[1:]) <= 128 and abs(scale) > 1e-35:   # (bf16's smallest steps are 9e-41)
+        check_three(run(x, torch.bfloat16, scale=scale), exact(x, [MUON] * 5, scale=scale))
+
+
+@gpu
+@pytest.mark.parametrize("scale", [1e-36, 1e-30, 3e37])
+@pytest.mark.parametrize("b", [64, 200])
+def test_packed_scales_near_the_ends_of_fp32(b, scale):
+    scale = torch.tensor(scale, dtype=torch.float32).item()
+    x = gaussian((2, b, b), "f32")
+    x = x - x.transpose(1, 2)
+    iu = torch.triu_indices(b, b, 1, device="cuda")
+    u = x[:, iu[0], iu[1]].contiguous()
+    out = torch.empty_like(u)
+    poetx.orthogonalize_q(u, b, out, scale=scale)
+    got = torch.zeros_like(x)
+    got[:, iu[0], iu[1]] = out
+    check_three(got - got.transpose(1, 2), exact(x, [MUON] * 5, scale=scale))
