@@ -21,10 +21,11 @@
 // of their time.
 //
 // Precision. Operands are fp16 parts of scaled values with fp32 accumulation: x = hi + lo,
-// hi = fp16(x), lo = fp16(x - hi), which carries 22 bits. The scales are powers of two chosen on
-// the host from the range of the singular values after each step (X_0 has them in [0, 1]; the
-// quintic's range over an interval is known), so nothing overflows and the smallest entries that
-// matter stay normal numbers.
+// hi = fp16(x), lo = fp16(x - hi), which carries 22 bits. The scales are powers of two chosen
+// from the range of the singular values after each step (X_0 has them in [0, 1]; the quintic's range
+// over an interval is known), so nothing overflows and the smallest entries that matter stay
+// normal numbers. A matrix whose norm is below eps has a smaller interval and scales of its own, which
+// ns_prep_kernel finds; so every matrix has its row of factors in the workspace.
 //   fp32 results, and bf16 results of up to 128 rows: every product is hi hi + hi lo + lo hi (three
 //     passes over K), error a few 2^-22 of the result's size.
 //   other bf16 results: one pass for gram and square; the update of every step but the last reads X
@@ -90,10 +91,9 @@ struct Job {
   int exact, chunk;                    // three part products; then K blocks per accumulator
   int fmode, out_f32, vec;             // the caller's array: layout, type, rows start on 16 bytes
   void* out;
-  float out_scale;
+  const float* factors;                // per matrix: Factors of every step, then Plan::out
   long long um, un;                    // its rows and columns (of the result as computed)
   int *counter, *done, *err;           // tiles handed out; per matrix: epilogue warps finished
-  Factors step[kMaxSteps];
 };
 struct Maps {
   CUtensorMap xk[2], xr[2], xn[2];   // X: left operand, right operand read K- and N-major,
@@ -101,6 +101,9 @@ struct Maps {
   CUtensorMap ak, ar, as, am; // A: left and right operand, pieces
   CUtensorMap bk, bs, bm;     // B: left operand, pieces
 };
+
+static_assert(sizeof(Factors) == 5 * sizeof(float), "the epilogue indexes them as floats");
+__host__ __device__ constexpr int factors_per_matrix(int steps) { return 5 * steps + 1; }
 
 struct Work {
   int t, kind, g, mb, nb;
@@ -279,8 +282,8 @@ __device__ __forceinline__ void emit_maps(const CUtensorMap* out, const CUtensor
 }
 
 // The same piece to the caller's array: v f out_scale.
-__device__ __forceinline__ void emit_user(const Job& p, const float* v, float f, int g, int row0,
-                                          int col0, uint8_t* stage, int lane) {
+__device__ __forceinline__ void emit_user(const Job& p, const float* v, float f, float out_scale, int g,
+                                          int row0, int col0, uint8_t* stage, int lane) {
   if (p.fmode == kTransposed) {
     // 32 rows of the piece are 32 neighbours of one output row
     const int i = row0 + lane, left = (int)min((long long)64, p.un - col0);
@@ -290,12 +293,12 @@ __device__ __forceinline__ void emit_user(const Job& p, const float* v, float f,
         float* o = static_cast<float*>(p.out) + at;
 #pragma unroll
         for (int q = 0; q < 64; ++q, o += p.um)
-          if (q < left) *o = v[q] * f * p.out_scale;
+          if (q < left) *o = v[q] * f * out_scale;
       } else {
         __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
 #pragma unroll
         for (int q = 0; q < 64; ++q, o += p.um)
-          if (q < left) *o = __float2bfloat16_rn(v[q] * f * p.out_scale);
+          if (q < left) *o = __float2bfloat16_rn(v[q] * f * out_scale);
       }
     }
     return;
@@ -304,8 +307,8 @@ __device__ __forceinline__ void emit_user(const Job& p, const float* v, float f,
 #pragma unroll
   for (int u = 0; u < 16; ++u)
     *reinterpret_cast<float4*>(stage + lane * 256 + ((u ^ (lane & 15)) << 4)) =
-        make_float4(v[4 * u] * f * p.out_scale, v[4 * u + 1] * f * p.out_scale,
-                    v[4 * u + 2] * f * p.out_scale, v[4 * u + 3] * f * p.out_scale);
+        make_float4(v[4 * u] * f * out_scale, v[4 * u + 1] * f * out_scale,
+                    v[4 * u + 2] * f * out_scale, v[4 * u + 3] * f * out_scale);
   __syncwarp();
   auto unit = [&](int r, int u) {
     return *reinterpret_cast<const float4*>(stage + r * 256 + ((u ^ (r & 15)) << 4));
@@ -612,6 +615,10 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
       const int ns = segments(job, w), nk = ns * k.nk, head = head_blocks(job, ns, k.nk);
       const int row0 = w.mb * S::TM + (int)rank * 128 + quarter * 32;
       const int base0 = w.nb * TN + cbase;
+      // (asked for early: they arrive while the accumulators fill)
+      const float* fac = job.factors + (long long)w.g * factors_per_matrix(job.steps);
+      const float f = fac[5 * w.t + w.kind], fa = fac[5 * w.t + 3], da = fac[5 * w.t + 4];
+      const float scale = fac[5 * job.steps];
       // A's 64 columns from c on, for b A, into the stage (which the warp has finished with)
       auto load_a = [&](int c) {
         if (lane == 0) {
@@ -657,20 +664,18 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
       }
       if (!ok) break;
       const bool out = w.kind == kUpdate && w.last;
-      const float f = job.step[w.t].f[w.kind];
       if (out) {
 #pragma unroll
         for (int c = 0; c < COLS; c += 64) {
           // (nothing of a packed result lies below the diagonal)
           const int col0 = base0 + c;
           if (row0 < job.um && col0 < job.un && !(job.fmode == kPacked && col0 + 63 <= row0))
-            emit_user(job, v + c, f, w.g, row0, col0, stage, lane);
+            emit_user(job, v + c, f, scale, w.g, row0, col0, stage, lane);
         }
         continue;
       }
       if (w.kind == kSquare) {
         // v <- v f + A fa
-        const float fa = job.step[w.t].fa;
 #pragma unroll
         for (int c = 0; c < COLS; c += 64) {
           if (c > 0) load_a(c);
@@ -711,8 +716,8 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
         const int col0 = base0 + c;   // pieces wholly in the padding are not stored
         if (row0 < job.R && col0 < k.cols)
           emit_maps(to, to_mirror, v + c, w.kind == kSquare ? 1.f : f,
-                    w.kind == kSquare ? job.step[w.t].da : 0.f, parts, job.batch, w.g, row0, col0,
-                    mirror, w.kind == kUpdate ? 0x80008000u : 0u, smem_u32(stage), lane);
+                    w.kind == kSquare ? da : 0.f, parts, job.batch, w.g, row0, col0, mirror,
+                    w.kind == kUpdate ? 0x80008000u : 0u, smem_u32(stage), lane);
       }
       // publish: this warp's copies are complete, then the matrix's count goes up
       if (lane == 0) {
@@ -803,9 +808,14 @@ struct Prep {
   int f32, form, tall, vec, chunks, batch, tiles, tiles_c;
   long long m, n;            // the caller's matrix (Skew: m = n = b)
   int r, k, R, ld;           // the workspace's: r x k in R x ld
-  double eps, sx, norm_mult; // norm^2 = norm_mult * sum of the partials
+  double eps, norm_mult;     // norm^2 = norm_mult * sum of the partials
   const double* partial;
   __half* out;
+  float* factors;            // per matrix, see Job
+  int steps;
+  float scale;
+  float coeffs[3 * kMaxSteps];
+  Plan plan;                 // of matrices whose norm is eps or more
 };
 __global__ void __launch_bounds__(256) ns_prep_kernel(const __grid_constant__ Prep p) {
   __shared__ float tile[64][65];
@@ -815,7 +825,20 @@ __global__ void __launch_bounds__(256) ns_prep_kernel(const __grid_constant__ Pr
   double s = 0.0;
   for (int c = tid; c < p.chunks; c += 256) s += p.partial[(long long)g * p.chunks + c];
   s = block_sum(s);
-  const double f = p.sx / (sqrt(p.norm_mult * s) + p.eps);
+  const double norm = sqrt(p.norm_mult * s), sum = norm + p.eps;
+  const bool below = below_eps(norm, p.eps);
+  const double f = (below ? x0_scale(norm / sum) : p.plan.x0) / sum;
+  if (blockIdx.x == 0) {
+    float* fac = p.factors + (long long)g * factors_per_matrix(p.steps);
+    if (!below) {
+      const float* all = reinterpret_cast<const float*>(p.plan.step);
+      for (int i = tid; i < 5 * p.steps; i += 256) fac[i] = all[i];
+      if (tid == 0) fac[5 * p.steps] = p.plan.out;
+    } else if (tid == 0) {
+      plan_from(norm / sum, p.coeffs, p.steps, p.scale, reinterpret_cast<Factors*>(fac),
+                fac + 5 * p.steps);
+    }
+  }
   const long long part = (long long)p.batch * p.R * p.ld;
   auto store8 = [&](int i, int j, const float (&v)[8]) {
     uint32_t h[4], l[4];
@@ -949,6 +972,7 @@ Dims dims_of(const Problem& p) {
 struct Ws {
   double* partial;
   int* counts;              // tiles handed out, then one count per matrix
+  float* factors;
   __half *x[2], *a, *b;
 };
 size_t layout(const Problem& p, void* base, Ws* o) {
@@ -957,6 +981,8 @@ size_t layout(const Problem& p, void* base, Ws* o) {
   Ws w;
   w.partial = static_cast<double*>(ar.take((size_t)p.batch * d.chunks * sizeof(double)));
   w.counts = static_cast<int*>(ar.take((size_t)(p.batch + 1) * sizeof(int)));
+  w.factors = static_cast<float*>(
+      ar.take((size_t)p.batch * factors_per_matrix(p.steps) * sizeof(float)));
   const size_t xb = (size_t)(2 * p.batch * d.R * d.ld) * 2;
   const size_t gb = (size_t)(2 * p.batch * d.R * d.R) * 2;
   w.x[0] = static_cast<__half*>(ar.take(xb));
@@ -1061,67 +1087,9 @@ cudaError_t launch(const Maps& maps, const Job& job, int sms, cudaStream_t s) {
 
 }  // namespace
 
-// ------------------------------------------------------------------ scales
-namespace {
-// The exponent of the power of two that brings values of at most `most` to between half of fp16's
-// range, 32768, and a half of that. (Nothing but zeros: any.)
-int scale_exponent(double most) {
-  if (!(most > 0.0)) return 0;
-  int k;
-  return std::frexp(most, &k) == 0.5 ? 16 - k : 15 - k;
-}
-}  // namespace
-
 bool make_plan(const Problem& p, Plan* plan) {
-  double top = 1.0;   // the singular values of X lie in [0, top]
-  int ex = scale_exponent(1.02 * top);
-  plan->x0 = ex;
-  for (int t = 0; t < p.steps; ++t) {
-    const double a = p.coeffs[3 * t], b = p.coeffs[3 * t + 1], c = p.coeffs[3 * t + 2];
-    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
-    // With l = s^2: B's eigenvalues a + b l + c l^2 and the next singular values
-    // s |a + b l + c l^2| over l in [0, top^2] have their extremes at the ends or where the
-    // derivatives b + 2 c l and a + 3 b l + 5 c l^2 vanish.
-    const double end = top * top;
-    double bb = std::fabs(a), x = 0.0;
-    auto look = [&](double l) {
-      if (!(l > 0.0 && l <= end)) return;
-      const double e = std::fabs(a + b * l + c * l * l);
-      bb = std::max(bb, e);
-      x = std::max(x, std::sqrt(l) * e);
-    };
-    look(end);
-    if (c != 0.0) {
-      look(-b / (2.0 * c));
-      const double disc = 9.0 * b * b - 20.0 * a * c;
-      if (disc >= 0.0) {
-        look((-3.0 * b + std::sqrt(disc)) / (10.0 * c));
-        look((-3.0 * b - std::sqrt(disc)) / (10.0 * c));
-      }
-    } else if (b != 0.0) {
-      look(-a / (3.0 * b));
-    }
-    // Entries of a matrix do not pass its spectral norm; 2 % for the rounding on the way. The scales
-    // follow the singular values down as well as up: fp16's smallest numbers would cut off the
-    // parts of what shrinks. The factors stay near 2^-15 all the same, since a polynomial's
-    // coefficients are bounded by its largest value; terms that vanish in fp32 vanish beside the others.
-    top = 1.02 * x;
-    const int ea = scale_exponent(1.02 * end), eb = scale_exponent(1.02 * bb);
-    const int next = scale_exponent(1.02 * top);
-    Factors& o = plan->step[t];
-    o.f[0] = (float)std::ldexp(1.0, ea - 2 * ex);
-    o.f[1] = (float)std::ldexp(c, eb - 2 * ea);
-    o.fa = (float)std::ldexp(b, eb - ea);
-    o.da = (float)std::ldexp(a, eb);
-    // The last update takes the operands' scales off and the caller's scale after them: their product
-    // can lie among fp32's smallest numbers where the result does not.
-    const int off = eb + ex, first = std::min(off, 100);
-    o.f[2] = (float)std::ldexp(1.0, t + 1 < p.steps ? next - off : -first);
-    plan->out = (float)std::ldexp((double)p.scale, first - off);
-    ex = next;
-    if (!(top < 1e6) || !(bb < 1e12)) return false;
-  }
-  return true;
+  plan->x0 = x0_scale(1.0);
+  return plan_from(1.0, p.coeffs, p.steps, p.scale, plan->step, &plan->out);
 }
 
 size_t workspace_bytes(const Problem& p) {
@@ -1155,8 +1123,10 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
     q.vec = !skew && !d.tall && p.n * (in_f32 ? 4 : 2) % 16 == 0;
     q.m = p.m; q.n = p.n;
     q.r = (int)d.r; q.k = (int)d.k; q.R = (int)d.R; q.ld = (int)d.ld;
-    q.eps = p.eps; q.sx = std::ldexp(1.0, plan.x0); q.norm_mult = skew ? 2.0 : 1.0;
+    q.eps = p.eps; q.norm_mult = skew ? 2.0 : 1.0;
     q.partial = w.partial; q.out = w.x[0];
+    q.factors = w.factors; q.steps = p.steps; q.scale = p.scale; q.plan = plan;
+    std::copy(p.coeffs, p.coeffs + 3 * p.steps, q.coeffs);
     // few blocks per matrix when there are many, each summing the norm's partials once
     const int64_t blocks = std::min<int64_t>(q.tiles, std::max<int64_t>(8, 148 * 8 / p.batch));
     TraceScope t("ns_prep", s);
@@ -1212,7 +1182,7 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
   job.chunk = d.R <= 512 ? 1 : 2;
   job.fmode = skew ? kPacked : d.tall ? kTransposed : kRows;
   job.out = out;
-  job.out_scale = plan.out;
+  job.factors = w.factors;
   job.out_f32 = out_f32;
   job.um = d.r;
   job.un = d.k;
@@ -1220,7 +1190,6 @@ cudaError_t run(const Problem& p, const Plan& plan, const void* x, void* out, vo
   job.counter = w.counts;
   job.done = w.counts + 1;
   job.err = err;
-  std::copy(plan.step, plan.step + p.steps, job.step);
   if (c.cg == 2) return launch<Shape<2, 256>>(maps, job, sms, s);
   return c.tn == 128 ? launch<Shape<1, 128>>(maps, job, sms, s)
                      : launch<Shape<1, 64>>(maps, job, sms, s);

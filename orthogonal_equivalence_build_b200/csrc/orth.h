@@ -27,13 +27,14 @@ struct Problem {
 struct Factors {
   float f[3], fa, da;
 };
-// Powers of two that hold every operand of every step inside fp16 (see orth.cu).
+// Powers of two that hold every operand of every step inside fp16 (see plan_from in orth_mma.cuh).
 struct Plan {
-  int x0;                  // X_0 is stored times 2^x0
+  double x0;               // X_0 is stored times this
   Factors step[kMaxSteps]; // (the last update's f leaves the result itself, or 2^j times it)
   float out;               // the caller's scale, times 2^-j
 };
-// false: the coefficients are not finite or let the singular values grow past every bound
+// For matrices of a norm of eps and more. false: the coefficients are not finite or let the singular
+// values grow past every bound
 bool make_plan(const Problem& p, Plan* plan);
 
 // One CTA per matrix (orth_small.cu), where a matrix fits into shared memory.

@@ -42,6 +42,75 @@ __device__ __forceinline__ void put(void* out, long long at, float x, int f32) {
   else static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(x);
 }
 
+// ------------------------------------------------------------------ scales
+// The exponent of the power of two that brings values of at most `most` to between half of fp16's
+// range, 32768, and a half of that. (Nothing but zeros: any.)
+__host__ __device__ inline int scale_exponent(double most) {
+  if (!(most > 0.0)) return 0;
+  int k;
+  return frexp(most, &k) == 0.5 ? 16 - k : 15 - k;
+}
+
+// The scale of X_0 and the factors of every step for singular values of X_0 in [0, top].
+__host__ __device__ inline double x0_scale(double top) {
+  return ldexp(1.0, scale_exponent(1.02 * top));
+}
+__host__ __device__ inline bool plan_from(double top, const float* coeffs, int steps, float scale,
+                                          Factors* step, float* out) {
+  int ex = scale_exponent(1.02 * top);
+  for (int t = 0; t < steps; ++t) {
+    const double a = coeffs[3 * t], b = coeffs[3 * t + 1], c = coeffs[3 * t + 2];
+    if (!isfinite(a) || !isfinite(b) || !isfinite(c)) return false;
+    // With l = s^2: B's eigenvalues a + b l + c l^2 and the next singular values
+    // s |a + b l + c l^2| over l in [0, top^2] have their extremes at the ends or where the
+    // derivatives b + 2 c l and a + 3 b l + 5 c l^2 vanish.
+    const double end = top * top;
+    double bb = fabs(a), x = 0.0;
+    auto look = [&](double l) {
+      if (!(l > 0.0 && l <= end)) return;
+      const double e = fabs(a + b * l + c * l * l);
+      bb = fmax(bb, e);
+      x = fmax(x, sqrt(l) * e);
+    };
+    look(end);
+    if (c != 0.0) {
+      look(-b / (2.0 * c));
+      const double disc = 9.0 * b * b - 20.0 * a * c;
+      if (disc >= 0.0) {
+        look((-3.0 * b + sqrt(disc)) / (10.0 * c));
+        look((-3.0 * b - sqrt(disc)) / (10.0 * c));
+      }
+    } else if (b != 0.0) {
+      look(-a / (3.0 * b));
+    }
+    // Entries of a matrix do not pass its spectral norm; 2 % for the rounding on the way. The scales
+    // follow the singular values down as well as up: fp16's smallest numbers would cut off the
+    // parts of what shrinks. The factors stay near 2^-15 all the same, since a polynomial's
+    // coefficients are bounded by its largest value; terms that vanish in fp32 vanish beside the others.
+    top = 1.02 * x;
+    const int ea = scale_exponent(1.02 * end), eb = scale_exponent(1.02 * bb);
+    const int next = scale_exponent(1.02 * top);
+    Factors& o = step[t];
+    o.f[0] = (float)ldexp(1.0, ea - 2 * ex);
+    o.f[1] = (float)ldexp(c, eb - 2 * ea);
+    o.fa = (float)ldexp(b, eb - ea);
+    o.da = (float)ldexp(a, eb);
+    // The last update takes the operands' scales off and the caller's scale after them: their product
+    // can lie among fp32's smallest numbers where the result does not.
+    const int off = eb + ex, first = off < 100 ? off : 100;
+    o.f[2] = (float)ldexp(1.0, t + 1 < steps ? next - off : -first);
+    *out = (float)ldexp((double)scale, first - off);
+    ex = next;
+    if (!(top < 1e6) || !(bb < 1e12)) return false;
+  }
+  return true;
+}
+
+// A matrix whose norm is below eps has no singular value near 1 after the division by norm + eps, and
+// its own scales: under those for [0, 1], fp16's smallest numbers would cut off its parts (with |X|_F =
+// 1e-5 eps fp32 results were 3e-5 off, with 1e-9 eps zeros). The plan of all others comes with the launch.
+__device__ __forceinline__ bool below_eps(double norm, double eps) { return norm > 0.0 && norm < eps; }
+
 // One lane of a converged warp, always the same one. The issuing warps run their loops with all
 // lanes and elect one for each copy, MMA and arrival: addresses and descriptors then are the same
 // in every lane and stay in uniform registers. With a loop of lane 0 alone a K block took 600

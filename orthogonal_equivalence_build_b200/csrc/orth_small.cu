@@ -11,7 +11,6 @@
 #include "orth_mma.cuh"
 
 #include <algorithm>
-#include <cmath>
 
 namespace poetx {
 namespace orth {
@@ -40,10 +39,11 @@ struct Small {
   int in_f32, out_f32, skew, tall, steps, fmode;
   int m, n, r, k;                      // the caller's matrix; as worked on, r <= k
   long long elems;                     // values of one matrix in the caller's arrays
-  double eps, sx;
-  float out_scale;
+  double eps;
+  float scale;
+  float coeffs[3 * kMaxSteps];
   int* err;
-  Factors step[kMaxSteps];
+  Plan plan;                           // of matrices whose norm is eps or more
 };
 
 __device__ __forceinline__ uint32_t at16(int i, int j) {   // byte of element (i, j) in a part
@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
   __shared__ uint64_t done_bar;
   __shared__ uint32_t tmem_holder;
   __shared__ int abort_flag;
+  __shared__ Plan plan;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* X = smem;
@@ -117,7 +118,15 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
     s += v * v;
   }
   s = block_sum(s);   // (its barriers also order the zeros before the values)
-  const double f0 = p.sx / (sqrt(p.skew ? 2.0 * s : s) + p.eps);
+  const double norm = sqrt(p.skew ? 2.0 * s : s), sum = norm + p.eps;
+  const bool below = below_eps(norm, p.eps);
+  const double f0 = (below ? x0_scale(norm / sum) : p.plan.x0) / sum;
+  if (!below) {
+    for (int i = tid; i < p.steps; i += kThreads) plan.step[i] = p.plan.step[i];
+    if (tid == 0) plan.out = p.plan.out;
+  } else if (tid == 0) {
+    plan_from(norm / sum, p.coeffs, p.steps, p.scale, plan.step, &plan.out);
+  }
   auto put_x = [&](int i, int j, float v) {
     const __half h = __float2half_rn(v);
     *reinterpret_cast<__half*>(X + at16(i, j)) = h;
@@ -178,13 +187,13 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
       }
       if (elect_one()) umma_commit(smem_u32(&done_bar));
     }
+    const float f = plan.step[t].f[kind], fa = plan.step[t].fa, da = plan.step[t].da;
     ok = wait_inline(smem_u32(&done_bar), phase, ctl, kErrMma);
     phase ^= 1u;
     ok = __syncthreads_and(ok);
     if (!ok) break;
     tc_fence_after();
     // columns past the result's padded width N (64 or 128) are not computed
-    const float f = p.step[t].f[kind], fa = p.step[t].fa, da = p.step[t].da;
     for (int c0 = half * (N / 2); c0 < (half + 1) * (N / 2); c0 += 32) {
       float v[32];
       {
@@ -215,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
       if (out) {
         float* stage = reinterpret_cast<float*>(A);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) stage[row * kOutLd + c0 + c] = v[c] * p.out_scale;
+        for (int c = 0; c < 32; ++c) stage[row * kOutLd + c0 + c] = v[c] * plan.out;
         continue;
       }
       uint8_t* to = kind == kGram ? A : kind == kSquare ? B : X;
@@ -301,11 +310,11 @@ cudaError_t run_small(const Problem& p, const Plan& plan, const void* x, void* o
   q.k = (int)std::max(p.m, p.n);
   q.elems = q.skew ? p.m * (p.m - 1) / 2 : p.m * p.n;
   q.eps = p.eps;
-  q.sx = std::ldexp(1.0, plan.x0);
-  q.out_scale = plan.out;
   q.err = device_error_word();
   if (!q.err) return cudaErrorUnknown;
-  std::copy(plan.step, plan.step + p.steps, q.step);
+  std::copy(p.coeffs, p.coeffs + 3 * p.steps, q.coeffs);
+  q.scale = p.scale;
+  q.plan = plan;
   cudaError_t e = cudaFuncSetAttribute(ns_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)kSmem);
   if (e != cudaSuccess) return e;

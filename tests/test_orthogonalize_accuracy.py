@@ -137,3 +137,47 @@ def test_packed_scales_near_the_ends_of_fp32(b, scale):
     got = torch.zeros_like(x)
     got[:, iu[0], iu[1]] = out
     check_three(got - got.transpose(1, 2), exact(x, [MUON] * 5, scale=scale))
+
+
+# ------------------------------------------------------------------------- norms below eps
+# X_0 is then small, and so may be everything after it; a result's elements are held to the same limits.
+@gpu
+@pytest.mark.parametrize("shape", [(6, 60, 100), (6, 200, 300), (6, 300, 150), (6, 24, 24)])
+@pytest.mark.parametrize("eps", [1e-7, 0.5])
+def test_norms_far_below_eps(shape, eps):
+    x = gaussian(shape, "f32")
+    for i, factor in enumerate((1e3, 1.0, 1e-3, 1e-6, 1e-10, 1e-20)):   # of eps, one matrix each
+        x[i] *= factor * eps / x[i].norm()
+    eps = torch.tensor(eps, dtype=torch.float32).item()
+    want = exact(x, [MUON] * 5, eps)
+    check_three(run(x, torch.float32, eps=eps), want)
+    if min(shape[1:]) <= 128:
+        check_three(run(x, torch.bfloat16, eps=eps), want)
+
+
+@gpu
+def test_norms_far_below_eps_that_grow_to_one():
+    # (1.875, -1.25, 0.375) lifts what is small by 1.875 a step and ends at the polar factor
+    x = gaussian((3, 60, 100), "f32")
+    for i, factor in enumerate((1.0, 1e-6, 1e-10)):
+        x[i] *= factor * 1e-7 / x[i].norm()
+    eps = torch.tensor(1e-7, dtype=torch.float32).item()
+    coeffs = [(1.875, -1.25, 0.375)] * 48
+    check_three(run(x, torch.float32, coeffs), exact(x, coeffs, eps))
+
+
+@gpu
+@pytest.mark.parametrize("b", [64, 200])
+def test_packed_norms_far_below_eps(b):
+    x = gaussian((4, b, b), "f32")
+    x = x - x.transpose(1, 2)
+    for i, factor in enumerate((1.0, 1e-3, 1e-6, 1e-10)):
+        x[i] *= factor * 1e-7 / x[i].norm()
+    iu = torch.triu_indices(b, b, 1, device="cuda")
+    u = x[:, iu[0], iu[1]].contiguous()
+    out = torch.empty_like(u)
+    poetx.orthogonalize_q(u, b, out)
+    got = torch.zeros_like(x)
+    got[:, iu[0], iu[1]] = out
+    eps = torch.tensor(1e-7, dtype=torch.float32).item()
+    check_three(got - got.transpose(1, 2), exact(x, [MUON] * 5, eps))
