@@ -327,12 +327,14 @@ poetx_status poetx_dequantize_w0(const int8_t* wq, const float* scale, int64_t m
  *   workspace >= poetx_orthogonalize_workspace_bytes(batch, m, n, steps) (0 for sizes that the call
  *   refuses or that need none: both sides at most 128); one workspace serves one call at a time.
  *   Errors: INVALID_ARG (NULL, negative size, steps, eps, scale, coefficients that are not finite
- *   or under which a singular value of [0, 1] passes 1e6), SHAPE (m or n > 65536, batch > 65535),
- *   DTYPE, ALIGN, WORKSPACE, CUDA.
+ *   or under which a singular value of [0, 1], with 2 % for rounding a step, passes 1e6), SHAPE (m
+ *   or n > 65536, batch > 65535, or 3 steps batch ceil(m / 128) ceil(n / 128) > 2^27 - 1), DTYPE,
+ *   ALIGN, WORKSPACE, CUDA.
  * poetx_orthogonalize_q — the same for an update of packed skew parameters: u and out
  *   [nblocks, b(b-1)/2] fp32 (a dq of poetx_linear_bwd, or its momentum); every block is taken as
  *   its skew b x b matrix (|X|_F^2 = 2 |u|^2), whose result is skew again. out may be u.
- *   2 <= b <= 1024. Accuracy as for F32 outputs. Otherwise as poetx_orthogonalize.
+ *   2 <= b <= 1024. Accuracy as for F32 outputs. Otherwise as poetx_orthogonalize with b for m and
+ *   n, its limits (1024 x 1024: 65535 blocks in at most 10 steps) included.
  * ------------------------------------------------------------------------------------------- */
 #define POETX_ORTH_MAX_STEPS 64
 size_t poetx_orthogonalize_workspace_bytes(int64_t batch, int64_t m, int64_t n, int32_t steps);
