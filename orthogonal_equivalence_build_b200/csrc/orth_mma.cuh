@@ -101,7 +101,7 @@ __host__ __device__ inline bool plan_from(double top, const float* coeffs, int s
     o.f[2] = (float)ldexp(1.0, t + 1 < steps ? next - off : -first);
     *out = (float)ldexp((double)scale, first - off);
     ex = next;
-    if (!(top < 1e6) || !(bb < 1e12)) return false;
+    if (!(top < 1e6)) return false;
   }
   return true;
 }

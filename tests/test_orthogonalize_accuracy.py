@@ -96,7 +96,8 @@ def test_bf16_results_of_coinciding_singular_values_round_once():
     [(0.001, 0.0, 0.0)] * 4 + [(1000.0, 0.0, 0.0)] * 4 + [MUON],
     [(1e-6, 0.0, 0.0), (1e5, 0.0, 0.0), (0.3, -0.2, 0.1)], [(0.0, 0.02, 0.0), (40.0, 0.0, 0.0)],
     [(0.0, 0.0, 1e-4)], [(1e-4, -3e-4, 1e-4), (0.0, 1e3, 0.0)],
-], ids=range(7))
+    [(1e-9, 0.0, 0.0), (1e13, 0.0, 0.0), (1e-4, 0.0, 0.0)],   # (a factor of B that is large by itself)
+], ids=range(8))
 def test_schedules_that_shrink_the_singular_values(shape, coeffs):
     x = gaussian(shape, "f32")
     check_three(run(x, torch.float32, coeffs), exact(x, coeffs))

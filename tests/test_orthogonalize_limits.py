@@ -56,3 +56,6 @@ def test_coefficients_within_the_bound_on_singular_values():
     # 2 % a step
     assert dense(1, 200, 64, [(1.0, 0.0, 0.0)] * 63 + [(2.8e5, 0.0, 0.0)]) == WORKSPACE
     assert dense(1, 200, 64, [(1.0, 0.0, 0.0)] * 63 + [(2.9e5, 0.0, 0.0)]) == INVALID
+    # what B is by itself has no bound
+    assert dense(1, 200, 64, [(1e-9, 0.0, 0.0), (1e13, 0.0, 0.0)]) == WORKSPACE
+    assert dense(1, 200, 64, [(1e-30, 0.0, 0.0), (3e34, 0.0, 0.0)]) == WORKSPACE
