@@ -528,6 +528,13 @@ def layer_norm_bwd(x: torch.Tensor, dy: torch.Tensor, gamma: Optional[torch.Tens
 # ----------------------------------------------------------------------------- Newton-Schulz
 # The quintic (a, b, c) that the Muon optimiser uses, for every step.
 MUON_COEFFS = (3.4445, -4.7750, 2.0315)
+ORTH_MAX_STEPS = 64
+
+
+def _check_steps(steps: int) -> None:
+    """The library refuses what is not in 1..ORTH_MAX_STEPS, but sees 32 bits of it only."""
+    if not -2 ** 31 <= steps < 2 ** 31:
+        raise ValueError(f"steps must be in 1..{ORTH_MAX_STEPS}")
 
 
 @functools.lru_cache(maxsize=64)
@@ -537,8 +544,9 @@ def _coeff_row(a: float, b: float, c: float, steps: int):
 
 def _coeff_array(coeffs, steps: int):
     """[steps][3] floats from one (a, b, c) or from one per step."""
+    _check_steps(steps)
     if len(coeffs) == 3 and not hasattr(coeffs[0], "__len__"):
-        return _coeff_row(*coeffs, max(steps, 0))
+        return _coeff_row(*coeffs, min(max(steps, 0), ORTH_MAX_STEPS))
     rows = [tuple(c) for c in coeffs]
     if len(rows) != steps or any(len(r) != 3 for r in rows):
         raise ValueError("coeffs must be one (a, b, c) or one per step")
@@ -553,6 +561,7 @@ def _matrices(x: torch.Tensor):
 
 def orthogonalize_workspace_bytes(x: torch.Tensor, out: torch.Tensor, steps: int = 5) -> int:
     batch, m, n = _matrices(x)
+    _check_steps(steps)
     return int(lib.poetx_orthogonalize_workspace_bytes(batch, m, n, steps))
 
 
@@ -573,6 +582,7 @@ def orthogonalize(x: torch.Tensor, out: torch.Tensor, steps: int = 5, coeffs=MUO
 
 
 def orthogonalize_q_workspace_bytes(nblocks: int, b: int, steps: int = 5) -> int:
+    _check_steps(steps)
     return int(lib.poetx_orthogonalize_q_workspace_bytes(nblocks, b, steps))
 
 

@@ -59,3 +59,19 @@ def test_coefficients_within_the_bound_on_singular_values():
     # what B is by itself has no bound
     assert dense(1, 200, 64, [(1e-9, 0.0, 0.0), (1e13, 0.0, 0.0)]) == WORKSPACE
     assert dense(1, 200, 64, [(1e-30, 0.0, 0.0), (3e34, 0.0, 0.0)]) == WORKSPACE
+
+
+def test_binding_passes_on_no_other_number_of_steps():
+    # ctypes keeps the low 32 bits of a number: 2^32 + 5 steps would be five
+    torch = pytest.importorskip("torch")
+    x, u = torch.zeros(200, 64), torch.zeros(1, 200 * 199 // 2)
+    for steps in (2 ** 32 + 5, 2 ** 31, -2 ** 32 + 5):
+        for call in (lambda: poetx.orthogonalize_workspace_bytes(x, x, steps),
+                     lambda: poetx.orthogonalize_q_workspace_bytes(1, 200, steps),
+                     lambda: poetx.orthogonalize(x, torch.empty_like(x), steps=steps),
+                     lambda: poetx.orthogonalize_q(u, 200, torch.empty_like(u), steps=steps)):
+            with pytest.raises(ValueError, match="steps"):
+                call()
+    # what the library refuses by itself needs no array of that size
+    assert len(poetx._coeff_array(MUON, 2 ** 31 - 1)) <= 3 * 65
+    assert poetx.orthogonalize_workspace_bytes(x, x, 65) == 0
