@@ -182,3 +182,100 @@ def test_packed_norms_far_below_eps(b):
     got[:, iu[0], iu[1]] = out
     eps = torch.tensor(1e-7, dtype=torch.float32).item()
     check_three(got - got.transpose(1, 2), exact(x, [MUON] * 5, eps))
+
+
+# ------------------------------------------------- every tile shape, layout and type, piece by piece
+# bf16 results of more than 128 rows come from partly single fp16 operands. The same emulation gives, before
+# the output's rounding, at most 1.15e-3 in norm and an element 8.5e-3 rms off (129 to 1100 rows). So an
+# element may be off by 2e-2 rms besides its own half step, and a matrix or a piece of 32 x 64 (what a warp
+# of the epilogue stores, as worked on) in norm by 1.2e-3 and the rounding's 2^-8 / sqrt(3): 4e-3. fp32
+# results: THREE, THREE_NORM, and three times that for a piece of a few thousand elements.
+LARGE, LARGE_NORM = 2e-2, 4e-3
+
+
+def check_pieces(got, want, few=False):
+    """got [batch, r, k] as worked on (r <= k); few: bf16 from three part products."""
+    err = got.double() - want
+    rms = want.square().mean((1, 2), keepdim=True).sqrt()
+    f32 = got.dtype == torch.float32
+    half, most = HALF_STEP[got.dtype], THREE if f32 or few else LARGE
+    over = err.abs() - (half * (1 + half) * want.abs() + most * rms)
+    assert over.max() <= 0, (over / rms).max().item()
+    norm = lambda t: t.flatten(1).norm(dim=1)
+    assert (norm(err) <= (THREE_NORM if f32 else LARGE_NORM) * norm(want)).all()
+    b, r, k = want.shape
+    cut = lambda t: t[:, :r // 32 * 32, :k // 64 * 64].reshape(b, r // 32, 32, k // 64, 64)
+    if r >= 32 and k >= 64:
+        e, w = (cut(t).square().sum((2, 4)).sqrt() for t in (err, want))
+        limit = 3 * THREE_NORM if f32 else LARGE_NORM
+        assert (e <= limit * w).all(), (e / w).max().item()
+
+
+def planted():
+    g = torch.Generator().manual_seed(3)
+    want = exact(torch.randn(1, 200, 320, generator=g), [MUON] * 5)
+    zero, one_part = want.clone(), want.clone()
+    zero[0, 64:96, 128:192] = 0
+    one_part[0, 64:96, 128:192] = one_part[0, 64:96, 128:192].half().double()
+    return want, zero, one_part
+
+
+def test_the_limits_see_a_lost_piece_and_a_lost_part():
+    want, zero, one_part = planted()
+    for t in (torch.float32, torch.bfloat16):
+        check_pieces(want.to(t), want)
+        with pytest.raises(AssertionError):
+            check_pieces(zero.to(t), want)
+    with pytest.raises(AssertionError):
+        check_pieces(one_part.float(), want)
+
+
+# in the order of the tiles that sizes lead to: pairs of 256 x 256, 128 x 128 of half of the symmetric
+# products, 128 x 128 of all, 128 x 64; tall ones are stored transposed, odd ones without vectors
+STACKS = [(3, 1500, 1550), (2, 1800, 1700), (8, 1000, 1003), (5, 1101, 1000), (1, 2305, 2303),
+          (1, 2048, 2048), (12, 700, 640), (60, 300, 700), (40, 333, 300), (6, 1024, 521),
+          (40, 250, 300), (40, 256, 256), (41, 300, 193), (2, 513, 2100),
+          (1, 1000, 333), (2, 300, 1001), (1, 129, 200), (1, 4096, 160), (3, 512, 512)]
+
+
+@gpu
+@pytest.mark.parametrize("shape", STACKS, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("xt,ot", [("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16"),
+                                   ("bf16", "f32")])
+def test_every_piece_of_a_stack(shape, xt, ot):
+    x = gaussian(shape, xt)
+    got, want = run(x, DT[ot]), exact(x, [MUON] * 5)
+    if shape[1] > shape[2]:
+        got, want = got.transpose(1, 2), want.transpose(1, 2)
+    check_pieces(got, want)
+
+
+@gpu
+@pytest.mark.parametrize("nb,b", [(5, 64), (3, 128), (1, 129), (4, 200), (40, 256), (9, 512), (1, 777),
+                                  (2, 1024), (12, 777), (36, 512), (16, 1000), (30, 1024)])
+def test_every_piece_of_packed_blocks(nb, b):
+    x = gaussian((nb, b, b), "f32")
+    x = x - x.transpose(1, 2)
+    iu = torch.triu_indices(b, b, 1, device="cuda")
+    u = x[:, iu[0], iu[1]].contiguous()
+    out = torch.full_like(u, 777.0)
+    poetx.orthogonalize_q(u, b, out)
+    torch.cuda.synchronize()
+    poetx.device_status()
+    got = torch.zeros_like(x)
+    got[:, iu[0], iu[1]] = out
+    check_pieces(got - got.transpose(1, 2), exact(x, [MUON] * 5))
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(2, 96, 200), (2, 400, 200), (3, 1000, 1100)])
+@pytest.mark.parametrize("ot", ["f32", "bf16"])
+@pytest.mark.parametrize("steps", [1, 2, 3, 8, 12])
+def test_step_counts_piece_by_piece(steps, ot, shape):
+    # (1.875, -1.25, 0.375) brings errors of the singular values down again, whatever the number of steps
+    coeffs = [(1.875, -1.25, 0.375)] * steps
+    x = gaussian(shape, "f32")
+    got, want = run(x, DT[ot], coeffs, scale=-0.5), exact(x, coeffs, scale=-0.5)
+    if shape[1] > shape[2]:
+        got, want = got.transpose(1, 2), want.transpose(1, 2)
+    check_pieces(got, want, few=min(shape[1:]) <= 128)
