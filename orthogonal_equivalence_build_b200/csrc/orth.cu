@@ -103,7 +103,8 @@ struct Maps {
 };
 
 static_assert(sizeof(Factors) == 5 * sizeof(float), "the epilogue indexes them as floats");
-__host__ __device__ constexpr int factors_per_matrix(int steps) { return 5 * steps + 1; }
+// floats of a matrix's row; the same for every number of steps, and so is the workspace's size beyond one
+constexpr int kFactors = 5 * kMaxSteps + 1;
 
 struct Work {
   int t, kind, g, mb, nb;
@@ -616,7 +617,7 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Job job) {
       const int row0 = w.mb * S::TM + (int)rank * 128 + quarter * 32;
       const int base0 = w.nb * TN + cbase;
       // (asked for early: they arrive while the accumulators fill)
-      const float* fac = job.factors + (long long)w.g * factors_per_matrix(job.steps);
+      const float* fac = job.factors + (long long)w.g * kFactors;
       const float f = fac[5 * w.t + w.kind], fa = fac[5 * w.t + 3], da = fac[5 * w.t + 4];
       const float scale = fac[5 * job.steps];
       // A's 64 columns from c on, for b A, into the stage (which the warp has finished with)
@@ -829,7 +830,7 @@ __global__ void __launch_bounds__(256) ns_prep_kernel(const __grid_constant__ Pr
   const bool below = below_eps(norm, p.eps);
   const double f = (below ? x0_scale(norm / sum) : p.plan.x0) / sum;
   if (blockIdx.x == 0) {
-    float* fac = p.factors + (long long)g * factors_per_matrix(p.steps);
+    float* fac = p.factors + (long long)g * kFactors;
     if (!below) {
       const float* all = reinterpret_cast<const float*>(p.plan.step);
       for (int i = tid; i < 5 * p.steps; i += 256) fac[i] = all[i];
@@ -982,7 +983,7 @@ size_t layout(const Problem& p, void* base, Ws* o) {
   w.partial = static_cast<double*>(ar.take((size_t)p.batch * d.chunks * sizeof(double)));
   w.counts = static_cast<int*>(ar.take((size_t)(p.batch + 1) * sizeof(int)));
   w.factors = static_cast<float*>(
-      ar.take((size_t)p.batch * factors_per_matrix(p.steps) * sizeof(float)));
+      ar.take((size_t)p.batch * kFactors * sizeof(float)));
   const size_t xb = (size_t)(2 * p.batch * d.R * d.ld) * 2;
   const size_t gb = (size_t)(2 * p.batch * d.R * d.R) * 2;
   w.x[0] = static_cast<__half*>(ar.take(xb));

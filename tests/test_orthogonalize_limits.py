@@ -75,3 +75,9 @@ def test_binding_passes_on_no_other_number_of_steps():
     # what the library refuses by itself needs no array of that size
     assert len(poetx._coeff_array(MUON, 2 ** 31 - 1)) <= 3 * 65
     assert poetx.orthogonalize_workspace_bytes(x, x, 65) == 0
+
+
+def test_a_workspace_serves_every_number_of_steps_beyond_one():
+    for args in ((1, 200, 64), (3, 1000, 333), (36, 512, 512)):
+        two = poetx.lib.poetx_orthogonalize_workspace_bytes(*args, 2)
+        assert all(poetx.lib.poetx_orthogonalize_workspace_bytes(*args, s) == two for s in (5, 8, 64))
