@@ -10,8 +10,12 @@
 // deviations' own mean dm corrects the first one's rounding: mean = first + dm,
 // var = sum d^2 / m - dm^2, x - mean = d - dm. Column sums are taken
 // per range of rows and the ranges added in order: no atomics, the same bits on every run.
-// Memory bound: each kernel reads its inputs once from HBM. No input is read through the read-only
-// cache: a block may start before the kernel that writes the input has ended.
+// Memory bound: the kernels of rows in registers and of rows through a ring read their inputs once
+// from HBM. Rows too wide for them (forward: more than 16384 columns; backward: also fp32 rows of more than
+// about 14300, of which two do not fit the ring) are read again for each sum, x and dy by a launch for
+// the column sums besides: 2048 x 20000 bf16 161 us forward, 212 us backward, of 25 and 38 us for the
+// bytes. No input is read through the read-only cache: a block may start before the kernel that
+// writes the input has ended.
 #include "norm.h"
 #include "umma_ptx.cuh"
 
@@ -152,7 +156,9 @@ __global__ void __launch_bounds__(kThreads) ln_cols_any_kernel(const Bwd a) {
 }
 
 // dgamma and dbeta: the ranges' sums, 32 columns per block; 32 threads of a column take every 32nd
-// range, and their sums are added by a fixed tree.
+// range, and their sums are added by a fixed tree. A launch of its own, since it needs every block's
+// sums: the last block to finish could take them, but would be known by a counter only, which has
+// to be zero before every call. With few rows it costs most: 256 x 512 fp32 5.9 us for both.
 __global__ void __launch_bounds__(1024) ln_cols_sum_kernel(const Bwd a) {
   __shared__ float sg[32][33], sb[32][33];
   pdl_wait();
@@ -525,7 +531,9 @@ cudaError_t launch_odd(const Fwd& a, cudaStream_t s) {
 }
 // Few elements a lane and many warps a row: single-element loads wait one by one otherwise (32 a lane
 // and a warp per row: 16384 x 1023 fp32 39 us against 25 us of 8 a lane, 1777 x 1023 9.8 against 5.4).
-// Beyond 2048 columns 16 a lane (8192 x 4095 bf16 54 us against 61 us of 8 and 512 threads).
+// Beyond 2048 columns 16 a lane (8192 x 4095 bf16 54 us against 61 us of 8 and 512 threads). The loads
+// count, not the bytes: bf16 rows take as long as fp32 ones (16384 x 1023 25 us, bytes 10.4; 8192 x 4095 53,
+// bytes 20.8; 4096 x 8191 72, bytes 20.8).
 template <typename T, typename WT>
 cudaError_t fwd_odd(const Fwd& a, cudaStream_t s) {
   if (a.m <= 256) return launch_odd<T, WT, 8, 1>(a, s);
@@ -1012,7 +1020,9 @@ __global__ void __launch_bounds__(512, 1) ln_bwd_wide_kernel(const Bwd a, const 
 constexpr int kMaxParts = 148;   // one block per SM
 
 // Shape of the one-pass backward for a width; stages < 2: a row is too wide for the ring. E = 8 up to
-// 5120 columns (at most 640 threads of 96 registers), 16 up to 8192 (8192 x 8192 bf16 86 us; 1024
+// 5120 columns: 640 threads are five warps a scheduler of 96 registers each (8192 x 5120 bf16 58 us, with
+// E = 16 71 us); the next warp is the sixth on one, which leaves 80 registers, and they spill (8192 x
+// 5376 bf16 102 us, with E = 16 72 us). 16 up to 8192 (8192 x 6144, 7168, 8192 bf16 74, 82, 85 us; 1024
 // threads of 8 columns and 64 registers spill: 145 us), 32 beyond. `sets` sets of threads and R rows
 // each make a group: at most 96 KB of x and dy, no more than leaves a group for every SM. R = 2 with
 // E = 8 (8192 x 5120 bf16 58.5 us against 67 us of one row; four rows spill: 16384 x 4096 bf16
@@ -1027,7 +1037,7 @@ GroupShape group_shape(int64_t T, int64_t m, int esz) {
   sh.E = m <= 5120 ? 8 : m <= 8192 ? 16 : 32;
   sh.threads = 32 * (int)((m + 32 * sh.E - 1) / (32 * sh.E));
   const int most = sh.E == 8 ? 2 : 1;
-  const int64_t fit = 96 * 1024 / (2 * m * esz);                  // rows in 64 KB
+  const int64_t fit = 96 * 1024 / (2 * m * esz);                  // rows in 96 KB
   const int64_t share = (T + kMaxParts - 1) / kMaxParts;          // rows per SM
   const int64_t rows = std::max<int64_t>(1, std::min(fit, share));
   sh.R = most;
