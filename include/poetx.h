@@ -354,9 +354,10 @@ poetx_status poetx_orthogonalize_q(const float* u, int64_t nblocks, int64_t b, c
  *     y = (x - mean) rstd gamma + beta.
  *   x [T, m] and y [T, m] have `dtype`; y may be x. gamma, beta [m] have `w_dtype`; NULL stands
  *   for ones and zeros. mean, rstd [T] fp32 outputs for the backward (either may be NULL).
- *   m <= 2^20, T m <= 2^50 (rows need not be a multiple of anything); sums are fp32, y is rounded
- *   once. A row that holds NaN or infinity gives NaN in that row only; a constant row gives beta
- *   up to rounding (with eps = 0 the formula is 0 / 0 there).
+ *   m <= 2^20, T m <= 2^50 (rows need not be a multiple of anything); y is rounded once. Sums are
+ *   fp32, those of the squares too: deviations past about 1e19 / sqrt(m) overflow them (rstd = 0), and
+ *   squares below 1e-38 lose digits. A row that holds NaN or infinity gives NaN in that row only; a
+ *   constant row gives beta up to rounding (with eps = 0 the formula is 0 / 0 there).
  *   Errors: INVALID_ARG (NULL x or y, negative size, eps negative or not finite), SHAPE, DTYPE,
  *   ALIGN, CUDA.
  * poetx_layer_norm_bwd — its exact gradient for upstream dy [T, m], given the forward's x, mean

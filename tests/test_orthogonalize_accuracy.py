@@ -279,3 +279,52 @@ def test_step_counts_piece_by_piece(steps, ot, shape):
     if shape[1] > shape[2]:
         got, want = got.transpose(1, 2), want.transpose(1, 2)
     check_pieces(got, want, few=min(shape[1:]) <= 128)
+
+
+# --------------------------------------------------------------------------- shapes at the ends
+@gpu
+@pytest.mark.parametrize("shape", [(500, 129, 1), (500, 1, 130), (3, 2, 5000), (2, 5000, 2),
+                                   (1, 1, 65536), (1, 65536, 1), (2, 40, 20000), (65535, 2, 3),
+                                   (2000, 33, 140)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("ot", ["f32", "bf16"])
+def test_thin_matrices_and_long_stacks(shape, ot):
+    x = gaussian(shape, "bf16")
+    check_three(run(x, DT[ot]), exact(x, [MUON] * 5))
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(5, 400, 190), (40, 300, 250), (12, 700, 640), (8, 1000, 1003)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("ot", ["f32", "bf16"])
+def test_zero_and_nonfinite_matrices_of_every_tile_shape(shape, ot):
+    x = gaussian(shape, "f32")
+    want = exact(x, [MUON] * 5)
+    x[1] = 0
+    x[2, 3, 5] = float("nan")
+    x[3, shape[1] - 1, shape[2] - 1] = -float("inf")
+    out = run(x, DT[ot])
+    assert torch.equal(out[1], torch.zeros_like(out[1]))
+    assert torch.isnan(out[2]).all() and torch.isnan(out[3]).all()
+    pick = [0] + list(range(4, shape[0]))
+    got, want = out[pick], want[pick]
+    if shape[1] > shape[2]:
+        got, want = got.transpose(1, 2), want.transpose(1, 2)
+    check_pieces(got, want)
+    # without eps, zeros are 0 / 0
+    assert torch.isnan(run(x[:2].contiguous(), DT[ot], eps=0.0)[1]).all()
+
+
+@gpu
+@pytest.mark.parametrize("b", [200, 512])
+def test_nonfinite_and_zero_packed_blocks_of_many_rows(b):
+    g = torch.Generator().manual_seed(b)
+    u = torch.randn(5, b * (b - 1) // 2, generator=g).cuda()
+    clean, out = torch.empty_like(u), torch.empty_like(u)
+    poetx.orthogonalize_q(u, b, clean)
+    u[1] = 0
+    u[2, 17] = float("nan")
+    u[3, -1] = float("inf")
+    poetx.orthogonalize_q(u, b, out)
+    assert torch.equal(out[[0, 4]], clean[[0, 4]])
+    assert torch.equal(out[1], torch.zeros_like(out[1]))
+    assert torch.isnan(out[2]).all() and torch.isnan(out[3]).all()
