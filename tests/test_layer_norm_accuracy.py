@@ -98,3 +98,38 @@ def test_rows_with_an_offset(T, m, dt, offset):
     torch.cuda.synchronize()
     for got, want in zip((y, mean, rstd), limits(x, gamma, beta, dt)):
         assert inside(got, want)
+
+
+@gpu
+@pytest.mark.parametrize("m", [4096, 4099, 20000])
+def test_more_than_two_to_the_31_values(m):
+    T = 2 ** 31 // m + 700
+    x, dy = (torch.empty(T, m, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for i in range(0, T, 50000):
+        for t in (x, dy):
+            t[i:i + 50000] = torch.randn(min(50000, T - i), m, device="cuda")
+    gamma, beta = 1 + 0.2 * torch.randn(m, device="cuda"), 0.2 * torch.randn(m, device="cuda")
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    dgamma, dbeta = torch.empty(m, device="cuda"), torch.empty(m, device="cuda")
+    poetx.layer_norm_fwd(x, gamma, beta, y, mean, rstd, eps=EPS)
+    poetx.layer_norm_bwd(x, dy, gamma, mean, rstd, dx, dgamma, dbeta)
+    torch.cuda.synchronize()
+    poetx.device_status()
+    # the first rows, and those around and behind element 2^31
+    pick = torch.cat([torch.arange(50), torch.arange(2 ** 31 // m - 50, 2 ** 31 // m + 50),
+                      torch.arange(T - 50, T)]).cuda()
+    for got, want in zip((y[pick], mean[pick], rstd[pick]),
+                         limits(x[pick].cpu(), gamma.cpu(), beta.cpu(), "bf16")):
+        assert inside(got, want)
+    # the same rows alone
+    part, dg, db = torch.empty_like(x[pick]), torch.empty_like(dgamma), torch.empty_like(dbeta)
+    poetx.layer_norm_bwd(x[pick], dy[pick], gamma, mean[pick], rstd[pick], part, dg, db)
+    assert torch.equal(part, dx[pick])
+    # column sums in 64 bits, each thread's share of the rows in fp32: at most T / 148 additions in a row
+    want, size = (torch.zeros(m, dtype=torch.float64, device="cuda") for _ in range(2))
+    for i in range(0, T, 20000):
+        d = dy[i:i + 20000].double()
+        want += d.sum(0)
+        size += d.abs().sum(0)
+    assert ((dbeta.double() - want).abs() <= (T / 148 + 200) * U * size).all()

@@ -328,3 +328,33 @@ def test_nonfinite_and_zero_packed_blocks_of_many_rows(b):
     assert torch.equal(out[[0, 4]], clean[[0, 4]])
     assert torch.equal(out[1], torch.zeros_like(out[1]))
     assert torch.isnan(out[2]).all() and torch.isnan(out[3]).all()
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(4, 200, 300), (4, 640, 400)])
+@pytest.mark.parametrize("factor,coeffs", [(1e-3, [MUON] * 5), (1e-10, [MUON] * 5),
+                                           (1e3, [(0.001, 0.0, 0.0)] * 3),
+                                           (1e-6, [(0.01, 0.0, 0.0), (300.0, 0.0, 0.0), MUON])])
+def test_small_iterates_of_large_bf16_results(shape, factor, coeffs):
+    x = gaussian(shape, "f32")
+    x *= factor * 1e-7 / x.flatten(1).norm(dim=1)[:, None, None]
+    eps = torch.tensor(1e-7, dtype=torch.float32).item()
+    got, want = run(x, torch.bfloat16, coeffs), exact(x, coeffs, eps)
+    if shape[1] > shape[2]:
+        got, want = got.transpose(1, 2), want.transpose(1, 2)
+    check_pieces(got, want)
+
+
+@gpu
+@pytest.mark.parametrize("shape,xt", [((1100, 1000, 2000), "bf16"), ((1100, 2003, 1000), "f32")])
+def test_stacks_of_more_than_two_to_the_31_values(shape, xt):
+    x = torch.empty(shape, dtype=DT[xt], device="cuda")
+    for i in range(0, shape[0], 100):
+        x[i:i + 100] = torch.randn(min(100, shape[0] - i), *shape[1:], device="cuda")
+    assert x.numel() > 2 ** 31
+    pick = [0, 1, shape[0] // 2, shape[0] - 1]
+    want = exact(x[pick], [MUON] * 5)
+    got = run(x, DT[xt])[pick]
+    if shape[1] > shape[2]:
+        got, want = got.transpose(1, 2), want.transpose(1, 2)
+    check_pieces(got, want)
