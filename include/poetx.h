@@ -323,7 +323,8 @@ poetx_status poetx_dequantize_w0(const int8_t* wq, const float* scale, int64_t m
  *   of the iteration; BF16 outputs with min(m, n) <= 128 the same, rounded once. Larger BF16 outputs
  *   come from operands that are partly single fp16 values: with the first coefficients above, in five
  *   steps, what is rounded in the end is off by about 1.1e-3 in norm over many different singular
- *   values, by up to 7e-3 where they all coincide.
+ *   values, by up to 1e-2 where few directions count (all singular values coincide, few rows are not
+ *   zero); one direction by itself by up to 2e-2. F32 outputs of BF16 inputs are free of that.
  *   Deterministic: the same inputs give the same bits.
  *   workspace >= poetx_orthogonalize_workspace_bytes(batch, m, n, steps) (0 for sizes that the call
  *   refuses or that need none: both sides at most 128); one workspace serves one call at a time.

@@ -35,11 +35,13 @@
 //     directions in proportion and is not amplified. Against the exact result, in units of its
 //     rms: 1.4e-3 for an update of a few strong directions over a background (single-part X
 //     2.0e-3, and 9.5e-3 with a background of 3 % of the strongest); bf16 rounding alone is
-//     1.7e-3. That is an average over the directions, each of which one rounding of A or B may
-//     move by up to 7e-3: 1.1e-3 of Gaussian matrices of 128 rows and more, but 1.7e-3 of 64 rows
-//     and 6e-3 of two, and 7e-3 of any size where all singular values coincide. Three passes for
-//     every size would be free of it and take 1.3 (200 x 300) to 2.2 times as long (4096 x 14336 11.0
-//     ms against 5.1 ms); up to 128 rows they take 1.2 to 1.3 times (64 x 300 104 us against 82).
+//     1.7e-3. That is an average over the directions, each of which the roundings may move by up to
+//     2e-2: 1.1e-3 of Gaussian matrices of 128 rows and more, but 1.7e-3 of 64 rows and 6e-3 of
+//     two; 8e-3 of more rows where all singular values coincide, and 1e-2 where but a few rows are not
+//     zero. No single rounding makes it (with X, A or B alone in two parts 1.2e-2 to 2.2e-2 are left of
+//     2e-2); three passes for every size would be free of it and take 1.3 (200 x 300) to 2.2 times
+//     as long (4096 x 14336 11.0 ms against 5.1 ms); up to 128 rows they take 1.2 to 1.3 times (64 x
+//     300 104 us against 82).
 #include "orth_mma.cuh"
 
 #include <algorithm>

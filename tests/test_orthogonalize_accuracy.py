@@ -358,3 +358,16 @@ def test_stacks_of_more_than_two_to_the_31_values(shape, xt):
     if shape[1] > shape[2]:
         got, want = got.transpose(1, 2), want.transpose(1, 2)
     check_pieces(got, want)
+
+
+@gpu
+def test_large_bf16_results_of_few_directions():
+    # One direction by itself, on the parts and scales in 64 bits: at most 2.1e-2 off over a million singular
+    # values in [1/256, 1], and 1.03e-2 for the values 1 / sqrt(q) of q equal ones.
+    x = torch.zeros(40, 300, 500, device="cuda")
+    for i, q in enumerate(list(range(1, 30)) + [50, 64, 100, 128, 150, 200, 222, 256, 270, 299, 300]):
+        x[i, :q, :q] = torch.eye(q, device="cuda")
+    got, want = run(x.bfloat16(), torch.bfloat16).double(), exact(x, [MUON] * 5)
+    assert ((got - want).abs() <= (2.2e-2 + 2.0 ** -8) * want.abs()).all()
+    got = run(x.bfloat16(), torch.float32).double()   # three part products
+    assert ((got - want).abs() <= THREE * want.abs()).all()
